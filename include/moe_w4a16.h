@@ -30,7 +30,14 @@
  *       same activation, quantised once with gate.input_scale (up.input_scale
  *       must be NULL or the same pointer); the down projection's input is h
  *       rounded to bf16, quantised with down.input_scale.
+ *   MOE_FMT_INT8 -- 8-bit integers with scales for each token and channel (W8A8;
+ *       the pages have no counterpart): packed: int8 [E, out, in]; scales: fp32
+ *       [E, out], w = q * scale.  The activation entering the projection is
+ *       quantised to 8 bits row by row as moe_quantize_int8 does, the product is
+ *       an exact integer sum.  128 * 128 * in must stay below 2^31.
  *   MOE_FMT_BF16 -- plain bf16 [E, out, in] (used for the shared expert).
+ * Experts that are not quantised are multiplied, and trained, with the 16-bit
+ * products moe_grouped_mm, moe_grouped_mm_dgrad and moe_grouped_mm_wgrad.
  *
  * Conventions for every entry point:
  *   - All tensor pointers are caller-owned DEVICE memory on the current device.
@@ -87,7 +94,7 @@ typedef enum {
                                  maximum; that row's outputs are NaN        */
 } moe_status;
 
-typedef enum { MOE_FMT_INT4_G128 = 0, MOE_FMT_NVFP4 = 1, MOE_FMT_BF16 = 2 } moe_wfmt;
+typedef enum { MOE_FMT_INT4_G128 = 0, MOE_FMT_NVFP4 = 1, MOE_FMT_BF16 = 2, MOE_FMT_INT8 = 5 } moe_wfmt;
 
 /* One projection bank in the pages' fused layout [num_experts, out_dim, in_dim]. */
 typedef struct {
@@ -95,8 +102,8 @@ typedef struct {
     int32_t num_experts;      /* E (1 for the shared expert)                      */
     int32_t out_dim;          /* rows: F for gate/up, H for down                  */
     int32_t in_dim;           /* reduction length: H for gate/up, F for down      */
-    const void* packed;       /* INT4: int32[E,out,in/8]; NVFP4: u8[E,out,in/2]; BF16: bf16[E,out,in] */
-    const void* scales;       /* INT4: bf16[E,out,in/128]; NVFP4: u8 E4M3[E,out,in/16]; BF16: NULL   */
+    const void* packed;       /* INT4: int32[E,out,in/8]; NVFP4: u8[E,out,in/2]; BF16: bf16[E,out,in]; INT8: s8[E,out,in] */
+    const void* scales;       /* INT4: bf16[E,out,in/128]; NVFP4: u8 E4M3[E,out,in/16]; BF16: NULL; INT8: fp32[E,out]     */
     const float* global_scale;/* NVFP4: fp32[E]; otherwise NULL                    */
     const float* input_scale; /* NVFP4 W4A4: fp32[E], the activation global scale of
                                  each expert (quant_algo NVFP4 with an input_scale,
@@ -289,6 +296,42 @@ int moe_grouped_w4a16_down(const void* h_perm, const int32_t* expert_offsets,
                            const moe_qweight* down, void* y_perm,
                            void* ws, size_t ws_bytes, moe_stream_t stream);
 
+/* Both grouped calls take MOE_FMT_INT8 banks too (any H and F that are
+ * multiples of 128): the rows are quantised as by moe_quantize_int8 (gate/up:
+ * row row_slot[r] / top_k of x; a row that holds an infinity or a NaN records
+ * MOE_ERR_NONFINITE and its outputs are NaN), each product is
+ *     float(sum q[r,k] w[e,n,k]) * (row scale * channel scale)
+ * with an exact 32-bit sum, and the rest is as above.  The workspace sizes
+ * above are enough. */
+
+/* Products grouped by expert in 16 bits, for experts that are not quantised,
+ * and their gradients (the pages describe the experts' products, The shape;
+ * they have no counterpart to the gradients).  Rows [expert_offsets[e],
+ * expert_offsets[e+1]) belong to expert e, as moe_permute orders them; an
+ * expert may have no rows, and rows outside every expert are not written.
+ *   moe_grouped_mm:        y[r, n]  = sum_k x[r, k] * w[e, n, k]
+ *   moe_grouped_mm_dgrad:  dx[r, k] = sum_n dy[r, n] * w[e, n, k]
+ *   moe_grouped_mm_wgrad:  dw[e, n, k] = sum over e's rows of dy[r, n] * x[r, k]
+ *                          (zero for an expert without rows); with accumulate
+ *                          the sums are added to dw, which must be fp32
+ * x, dx: [rows, in_dim]; y, dy: [rows, out_dim]; w, dw: [E, out_dim, in_dim];
+ * all of one 16-bit type (f16 = 0: bf16, 1: IEEE fp16), dw also fp32
+ * (dw_f32 = 1).  Sums are fp32, rounded once.  out_dim and in_dim are multiples
+ * of 8, E <= 1024, tensors 16-byte aligned and contiguous; rows is the row count
+ * of the tensors.  Offsets that decrease or leave [0, rows] are clipped to it
+ * and recorded as MOE_ERR_DEVICE_INDEX.  Results do not depend on the order in
+ * which tiles run.  ws: at least 1024 bytes (the control block), zero-filled
+ * once; it holds no intermediate results. */
+int moe_grouped_mm(const void* x, const int32_t* expert_offsets, int rows, const void* w, int E,
+                   int out_dim, int in_dim, int f16, void* y, void* ws, size_t ws_bytes,
+                   moe_stream_t stream);
+int moe_grouped_mm_dgrad(const void* dy, const int32_t* expert_offsets, int rows, const void* w, int E,
+                         int out_dim, int in_dim, int f16, void* dx, void* ws, size_t ws_bytes,
+                         moe_stream_t stream);
+int moe_grouped_mm_wgrad(const void* dy, const void* x, const int32_t* expert_offsets, int rows, int E,
+                         int out_dim, int in_dim, int f16, void* dw, int dw_f32, int accumulate,
+                         void* ws, size_t ws_bytes, moe_stream_t stream);
+
 /* Unpermute and combine ("Step 5 Preview: 92 narrow layers...", The shape:
  * a token's output is its shared expert plus its 8 routed experts; the
  * routing weight was applied by the down projection):
@@ -361,6 +404,15 @@ int moe_quantize_nvfp4_act(const void* x, int64_t rows, int64_t cols, const floa
  * scales: bf16 [rows, cols/128] (out). */
 int moe_quantize_int4_g128(const void* w, int64_t rows, int64_t cols, int32_t* packed,
                            void* scales, moe_stream_t stream);
+
+/* 8-bit quantiser of rows (weights: a row is a channel; activations: a token).
+ * Row r of x (bf16, or fp16 with f16 = 1, [rows, cols], cols % 16 == 0):
+ *     scales[r] = max|x| / 127 (fp32),  codes[r, c] = rint(127 x / max|x|),
+ * ties to even, codes in [-127, 127].  A zero row has scale 0 and zero codes; a
+ * row that holds an infinity or a NaN has scale NaN and zero codes.
+ * codes: int8 [rows, cols] (out); scales: fp32 [rows] (out). */
+int moe_quantize_int8(const void* x, int64_t rows, int64_t cols, int f16, int8_t* codes,
+                      float* scales, moe_stream_t stream);
 
 /* NVFP4 quantiser ("Step-5-Preview-NVFP4-Local", Format): per matrix,
  * global = amax / (6 * 448) (fp32); per block of 16 along cols,

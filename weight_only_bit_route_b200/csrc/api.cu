@@ -6,6 +6,7 @@
 #include <mutex>
 #include <vector>
 
+#include "grouped_mm.cuh"
 #include "moe_internal.cuh"
 
 using namespace moe;
@@ -27,13 +28,17 @@ int check_dims(int T, int H, int E, int F, int k) {
     return MOE_OK;
 }
 
+// 8-bit products accumulate in 32 bits: 128 * 128 * in must stay below 2^31
+constexpr int kInt8MaxIn = 131072;
+
 int check_bank(const moe_qweight* b, int E, int out, int in) {
     if (!b) return MOE_ERR_INVALID_ARG;
     if (b->input_scale && b->fmt != MOE_FMT_NVFP4) return MOE_ERR_UNSUPPORTED;   // W4A4 is NVFP4 only
-    if (b->fmt != MOE_FMT_INT4_G128 && b->fmt != MOE_FMT_NVFP4 && b->fmt != MOE_FMT_BF16)
+    if (b->fmt != MOE_FMT_INT4_G128 && b->fmt != MOE_FMT_NVFP4 && b->fmt != MOE_FMT_BF16 && b->fmt != MOE_FMT_INT8)
         return MOE_ERR_UNSUPPORTED;
     if (b->num_experts != E || b->out_dim != out || b->in_dim != in) return MOE_ERR_INVALID_ARG;
     if (in % 128 || out <= 0) return MOE_ERR_UNSUPPORTED;
+    if (b->fmt == MOE_FMT_INT8 && in >= kInt8MaxIn) return MOE_ERR_UNSUPPORTED;
     if (!b->packed || !al16(b->packed)) return MOE_ERR_INVALID_ARG;
     if (b->fmt != MOE_FMT_BF16 && !b->scales) return MOE_ERR_INVALID_ARG;
     if (b->fmt == MOE_FMT_NVFP4 && !b->global_scale) return MOE_ERR_INVALID_ARG;
@@ -100,6 +105,23 @@ GemmBuffers gemm_buffers(void* base, int rows, int in_dim, bool act_ready, bool 
 bool i8_int4(const GemvProblem& p, int rows) {
     return p.fmt == MOE_FMT_INT4_G128 && p.E > 1 && rows <= kI8Int4MaxRows;
 }
+// A routed projection (or gate and up) in 8 bits: the rows are quantised into the pre-pass region (row scales, then
+// codes [rows, in]: part of what gemm_prep_bytes counts), then multiplied.
+int run_int8(const GemvProblem& p, bool gateup, int rows, int64_t nsrc, void* prep, cudaStream_t s) {
+    float* scales = reinterpret_cast<float*>(prep);
+    int8_t* codes = reinterpret_cast<int8_t*>(prep) + align256(size_t(rows) * 4);
+    MOE_TRY(launch_quant_int8(p.act, p.act_f16 != 0, rows, p.in_dim, p.act_by_token ? p.row_slot : nullptr, p.top_k,
+                              nsrc, p.offsets + p.E, codes, scales, p.status, s));
+    MmProblem m{};
+    m.act = codes; m.act_scale = scales;
+    m.w0 = p.p0; m.s0 = reinterpret_cast<const float*>(p.s0);
+    if (gateup) { m.w1 = p.p1; m.s1 = reinterpret_cast<const float*>(p.s1); }
+    m.offsets = p.offsets; m.row_slot = p.row_slot; m.topk_w = p.topk_w;
+    m.out = reinterpret_cast<uint16_t*>(p.out); m.status = p.status;
+    m.E = p.E; m.out_dim = p.out_dim; m.in_dim = p.in_dim; m.rows = rows;
+    m.i8 = true;
+    return launch_grouped_mm(m, s);
+}
 size_t step_scratch(int E, int fmt, bool gateup, int rows, int in_dim, int out_dim) {
     return grouped_scratch(E, rows, in_dim) + split_bytes(shared_ksplit(E, fmt, gateup, rows, in_dim), gateup, rows, out_dim);
 }
@@ -119,7 +141,7 @@ int layer_checks(const void* x, int T, const moe_layer* L, void* y, void* ws, si
     MOE_TRY(check_bank(&L->down, L->E, L->H, L->F));
     if (L->gate.fmt == MOE_FMT_BF16 || L->gate.fmt != L->up.fmt || L->gate.fmt != L->down.fmt)
         return MOE_ERR_UNSUPPORTED;
-    if (L->act_f16 && !(gemm_shape_ok(L->H, L->F) && gemm_shape_ok(L->F, L->H))) return MOE_ERR_UNSUPPORTED;
+    if (L->act_f16 && L->gate.fmt != MOE_FMT_INT8 && !(gemm_shape_ok(L->H, L->F) && gemm_shape_ok(L->F, L->H))) return MOE_ERR_UNSUPPORTED;
     // gate and up share one quantised activation (the gate's input scale)
     if (L->up.input_scale && L->up.input_scale != L->gate.input_scale) return MOE_ERR_UNSUPPORTED;
     if ((L->gate.input_scale || L->down.input_scale) && !(gemm_shape_ok(L->H, L->F) && gemm_shape_ok(L->F, L->H)))
@@ -232,7 +254,8 @@ int layer_run(const void* x, int T, const moe_layer* L, void* y, void* ws, cudaS
         MOE_TRY(launch_permute(ids, T, k, E, offsets, row_slot, slot_row, at<int32_t>(ws, W.hist), status, s));
     }
 
-    const bool routed_gemm = gemm_shape_ok(H, F) && gemm_shape_ok(F, H);
+    const bool int8 = L->gate.fmt == MOE_FMT_INT8;
+    const bool routed_gemm = !int8 && gemm_shape_ok(H, F) && gemm_shape_ok(F, H);
 
     GemvProblem gu{};
     gu.act = xb; gu.act_by_token = 1; gu.top_k = k; gu.offsets = offsets; gu.row_slot = row_slot;
@@ -247,7 +270,10 @@ int layer_run(const void* x, int T, const moe_layer* L, void* y, void* ws, cudaS
     dn.out = y_perm; dn.status = status; dn.in_scale = L->down.input_scale;
     // routed experts: both projections on one path
     const bool i8 = routed_gemm && i8_int4(gu, R);
-    if (routed_gemm) {
+    if (int8) {
+        MOE_TRY(run_int8(gu, true, R, T, prep, s));
+        MOE_TRY(run_int8(dn, false, R, R, prep, s));
+    } else if (routed_gemm) {
         // 16-bit gate/up activation rows are gathered into the y_perm region,
         // free until the down projection writes it
         GemmBuffers gb = gemm_buffers(prep, R, H, false, i8);
@@ -258,7 +284,8 @@ int layer_run(const void* x, int T, const moe_layer* L, void* y, void* ws, cudaS
     } else {
         MOE_TRY(launch_stream_gemv(gu, nullptr, true, T, prep, s, true));
     }
-    if (routed_gemm) {
+    if (int8) {
+    } else if (routed_gemm) {
         GemmBuffers db = gemm_buffers(prep, R, F, false, i8);
         db.sched = status + 8;
         db.max_expert_rows = T;
@@ -441,6 +468,7 @@ int moe_grouped_w4a16_swiglu(const void* x, int T, int H, const int32_t* expert_
     p.out = reinterpret_cast<__nv_bfloat16*>(h_perm); p.status = at<int32_t>(ws, 0);
     p.in_scale = gate->input_scale;
     void* prep = at<void>(ws, kStepScratch + align256(size_t(E + 2) * 16));
+    if (gate->fmt == MOE_FMT_INT8) return run_int8(p, true, rows, T, prep, cs(stream));
     GemmBuffers b = gemm_buffers(prep, rows, H, false, i8_int4(p, rows));
     b.sched = p.status + 8;
     b.max_expert_rows = T;
@@ -467,11 +495,59 @@ int moe_grouped_w4a16_down(const void* h_perm, const int32_t* expert_offsets, co
     p.out = reinterpret_cast<__nv_bfloat16*>(y_perm); p.status = at<int32_t>(ws, 0);
     p.in_scale = down->input_scale;
     void* prep = at<void>(ws, kStepScratch + align256(size_t(E + 2) * 16));
+    if (down->fmt == MOE_FMT_INT8) return run_int8(p, false, rows, rows, prep, cs(stream));
     // BF16 rows are read in place (row r is activation row r)
     GemmBuffers b = gemm_buffers(prep, rows, F, down->fmt == MOE_FMT_BF16, i8_int4(p, rows));
     b.sched = p.status + 8;
     b.max_expert_rows = rows;
     return run_problem(p, false, rows, rows, prep, b, step_partial(ws, E, rows, F), cs(stream));
+}
+
+namespace {
+// Checks shared by the 16-bit products (rows > 0: the row tensors are read)
+int check_mm(const void* r0, const void* r1, const void* big, const int32_t* offsets, int rows, int E, int out, int in,
+             void* ws, size_t ws_bytes) {
+    if (rows < 0 || E <= 0 || out <= 0 || in <= 0) return MOE_ERR_INVALID_ARG;
+    if (E > kMaxE || out % 8 || in % 8) return MOE_ERR_UNSUPPORTED;
+    if (!offsets || !big || !al16(big)) return MOE_ERR_INVALID_ARG;
+    if (rows > 0 && (!r0 || !r1 || !al16(r0) || !al16(r1))) return MOE_ERR_INVALID_ARG;
+    return check_ws(ws, ws_bytes, kStepScratch);
+}
+int run_mm(const void* act, const int32_t* offsets, int rows, const void* w, int E, int out, int in, int f16, void* y,
+           bool grad, void* ws, cudaStream_t s) {
+    MmProblem m{};
+    m.act = act; m.w0 = w; m.offsets = offsets; m.out = reinterpret_cast<uint16_t*>(y); m.status = at<int32_t>(ws, 0);
+    m.E = E; m.out_dim = out; m.in_dim = in; m.rows = rows;
+    m.f16 = f16 != 0; m.grad = grad;
+    return launch_grouped_mm(m, s);
+}
+}  // namespace
+
+int moe_grouped_mm(const void* x, const int32_t* expert_offsets, int rows, const void* w, int E, int out_dim,
+                   int in_dim, int f16, void* y, void* ws, size_t ws_bytes, moe_stream_t stream) {
+    MOE_TRY(check_mm(x, y, w, expert_offsets, rows, E, out_dim, in_dim, ws, ws_bytes));
+    if (rows == 0) return MOE_OK;
+    return run_mm(x, expert_offsets, rows, w, E, out_dim, in_dim, f16, y, false, ws, cs(stream));
+}
+
+int moe_grouped_mm_dgrad(const void* dy, const int32_t* expert_offsets, int rows, const void* w, int E, int out_dim,
+                         int in_dim, int f16, void* dx, void* ws, size_t ws_bytes, moe_stream_t stream) {
+    MOE_TRY(check_mm(dy, dx, w, expert_offsets, rows, E, out_dim, in_dim, ws, ws_bytes));
+    if (rows == 0) return MOE_OK;
+    return run_mm(dy, expert_offsets, rows, w, E, out_dim, in_dim, f16, dx, true, ws, cs(stream));
+}
+
+int moe_grouped_mm_wgrad(const void* dy, const void* x, const int32_t* expert_offsets, int rows, int E, int out_dim,
+                         int in_dim, int f16, void* dw, int dw_f32, int accumulate, void* ws, size_t ws_bytes,
+                         moe_stream_t stream) {
+    MOE_TRY(check_mm(dy, x, dw, expert_offsets, rows, E, out_dim, in_dim, ws, ws_bytes));
+    if (accumulate && !dw_f32) return MOE_ERR_UNSUPPORTED;      // a 16-bit sum would be rounded at every call
+    if (accumulate && rows == 0) return MOE_OK;
+    WgradProblem p{};
+    p.dy = dy; p.x = x; p.offsets = expert_offsets; p.dw = dw; p.status = at<int32_t>(ws, 0);
+    p.E = E; p.out_dim = out_dim; p.in_dim = in_dim; p.rows = rows;
+    p.f16 = f16 != 0; p.out_f32 = dw_f32 != 0; p.accumulate = accumulate != 0;
+    return launch_grouped_wgrad(p, cs(stream));
 }
 
 int moe_unpermute_combine(const void* y_perm, const int32_t* slot_row, int T, int top_k, int H,
@@ -609,6 +685,15 @@ int moe_quantize_int4_g128(const void* w, int64_t rows, int64_t cols, int32_t* p
     if (!w || !packed || !scales || !al16(w) || !al16(packed)) return MOE_ERR_INVALID_ARG;
     return launch_quant_int4(reinterpret_cast<const __nv_bfloat16*>(w), rows, cols, packed,
                              reinterpret_cast<__nv_bfloat16*>(scales), cs(stream));
+}
+
+int moe_quantize_int8(const void* x, int64_t rows, int64_t cols, int f16, int8_t* codes, float* scales,
+                      moe_stream_t stream) {
+    if (rows < 0 || cols < 0) return MOE_ERR_INVALID_ARG;
+    if (cols % 16 || rows > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    if (rows == 0 || cols == 0) return MOE_OK;
+    if (!x || !codes || !scales || !al16(x) || !al16(codes)) return MOE_ERR_INVALID_ARG;
+    return launch_quant_int8(x, f16 != 0, rows, cols, nullptr, 1, rows, nullptr, codes, scales, nullptr, cs(stream));
 }
 
 int moe_quantize_nvfp4_act(const void* x, int64_t rows, int64_t cols, const float* g, uint8_t* packed,

@@ -1,0 +1,442 @@
+// Matrix products grouped by expert, in 16 bits and in 8-bit integers, on the 5th-generation tensor cores.
+//
+// Rows offsets[e] to offsets[e+1] belong to expert e.  With W_e = w[e] stored [out, in]:
+//     forward   y[r, n]  = sum_k x[r, k] w[e, n, k]                     (K = in)
+//     gradient  dx[r, k] = sum_n dy[r, n] w[e, n, k]                    (K = out)
+//     int8      y[r, n]  = t s_r s_n sum_k q[r, k] w[e, n, k]           (s: row and channel scales, t: routing weight)
+//     int8 gate/up       h[r, f] = silu(g) u, g and u as above with two banks
+//
+// One kernel computes them all as D = A B with A the weights (M = 128 of their output features, 256 for a CTA
+// pair) and B the rows (N up to NT of one expert): an expert holds few rows more often than few features, and N
+// can be any multiple of 16, so little of a tile is padding.  The gradient reads the same stored weights along
+// the other axis: A's shared-memory tile is then stored along M (rows of 64 input features, one per output
+// feature) and the MMA descriptor says so; nothing is transposed.
+//
+// A tile is (expert, 128 * CG features, up to NT rows).  A persistent CTA (or pair) takes every grid-th tile;
+// every role computes the same sequence from a table of the experts' first tiles in shared memory, so nothing is
+// handed out through the workspace.  Warp roles:
+//   warp 0     TMA producer.  A stage is K = 128 bytes (64 elements of 16 bits, 128 of 8) of A and B, 128-byte
+//              swizzled; rows past the tensors' ends arrive as zeros, and so does K past its end on both sides.
+//   warp 1     issues the MMAs (in a pair: the first CTA's warp, for both) and commits each stage.
+//   warps 4-7  epilogue from tensor memory: lane = feature, column = row.  Two accumulator buffers, so that the
+//              epilogue of a tile overlaps the next tile's products.
+// B's rows behind the tile's last are other experts' rows: their columns are computed and never stored.
+//
+// Every wait is bounded (moe_set_wait_limit).  On expiry the kernel records MOE_ERR_TIMEOUT, stops issuing work,
+// waits (bounded) for its copies and MMAs in flight, frees its tensor memory and returns.
+#include <cstring>
+
+#include "grouped_mm.cuh"
+#include "mm_ptx.cuh"
+
+namespace moe {
+
+constexpr int MM_THREADS = 256;
+
+// Tile shape of one instantiation.  NT: rows per tile; CG: CTAs per tile.
+template <bool I8, bool AMN, bool GU, int NT, int CG>
+struct MmCfg {
+    static constexpr int kMat = GU ? 2 : 1;
+    static constexpr int kBK = I8 ? 128 : 64;                     // K per stage (128 bytes)
+    static constexpr int kABytes = 128 * 128;                     // per matrix
+    static constexpr int kBBytes = NT / CG * 128;
+    static constexpr int kStage = kMat * kABytes + kBBytes;
+    static constexpr int kRingBytes = 200 * 1024;                 // beside it: the tile table (16 bytes per expert)
+    static constexpr int kStages = kRingBytes / kStage < 12 ? kRingBytes / kStage : 12;
+    static constexpr int kAccCols = kMat * NT;                    // one accumulator buffer
+    static constexpr int kTmem = 2 * kAccCols <= 32 ? 32 : (2 * kAccCols <= 64 ? 64 : (2 * kAccCols <= 128 ? 128 : (2 * kAccCols <= 256 ? 256 : 512)));
+    static constexpr int kStep = 16 * CG;                         // a tile's N is a multiple of this
+    static_assert(2 * kAccCols <= 512 && NT % kStep == 0 && kStages >= 2, "tile shape");
+};
+
+struct MmTile { int e, m0, n0, nval, bn; };                       // n0: first row (of all rows)
+
+struct MmArgs {
+    CUtensorMap a0, a1;                  // weights [E][out][in]; a1: up (gate/up)
+    CUtensorMap b16, b64;                // rows, boxes of 16 and 64
+    const int32_t* offsets;
+    const int32_t* row_slot;             // int8: slot of a row (routing weight), nullable
+    const float* topk_w;
+    const float* act_scale;              // int8: [rows]
+    const float* s0; const float* s1;    // int8: channel scales [E][out]
+    uint16_t* out;                       // [rows][ldo]
+    int32_t* status;
+    int E, mdim, kdim, rows;             // mdim: output features (A's M), kdim: contraction length
+    int f16;                             // 16-bit elements are fp16 (else bf16)
+    int early;                           // the kernel before is this product's own row pass
+};
+
+template <bool I8, bool AMN, bool GU, int NT, int CG>
+__global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant__ MmArgs a) {
+    using C = MmCfg<I8, AMN, GU, NT, CG>;
+    constexpr int S = C::kStages;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ __align__(8) uint64_t full[S], empty[S], acc_full[2], acc_empty[2], drain, hold_bar;
+    __shared__ uint32_t s_tmem;
+    __shared__ uint32_t s_issued;                    // stages this CTA's producer has issued
+    __shared__ int s_wsum[MM_THREADS / 32], s_wt[MM_THREADS / 32], s_nact, s_total, s_hold;
+    __shared__ volatile GAbort s_ab;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = CG == 2 ? g_cta_rank() : 0u;
+    const int MT = (a.mdim + 128 * CG - 1) / (128 * CG);
+    const int KS = (a.kdim + C::kBK - 1) / C::kBK;
+
+    if (tid == 0) {
+        for (int s = 0; s < S; s++) {
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(g_smem(&full[s])), "r"(CG));
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(g_smem(&empty[s])));
+        }
+        for (int s = 0; s < 2; s++) {
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(g_smem(&acc_full[s])));
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(g_smem(&acc_empty[s])), "r"(4 * CG));
+        }
+        asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(g_smem(&drain)));
+        asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(g_smem(&hold_bar)));
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        s_ab.flag = 0;
+        s_issued = 0;
+    }
+    if (warp == 2) g_tmem_alloc<CG>(g_smem(&s_tmem), C::kTmem);
+    if (!a.early) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (tid == 0) {
+        s_ab.limit_ns = g_limit_from(a.status);
+        s_hold = g_hold_from(a.status);
+    }
+
+    uint8_t* ring = smem + ((1024u - (g_smem(smem) & 1023u)) & 1023u);
+    int4* tbl = reinterpret_cast<int4*>(ring + S * C::kStage);      // active experts: {expert, first tile, first row, rows}
+    {
+        constexpr int PER = kMaxE / MM_THREADS;
+        int eb[PER], ne[PER], nt[PER], local = 0, ltiles = 0;
+#pragma unroll
+        for (int i = 0; i < PER; i++) {
+            const int e = tid * PER + i;
+            eb[i] = 0;
+            ne[i] = 0;
+            if (e < a.E) mm_expert_rows(a.offsets, e, a.rows, a.status, eb[i], ne[i]);
+            nt[i] = ((ne[i] + NT - 1) / NT) * MT;
+            local += ne[i] > 0;
+            ltiles += nt[i];
+        }
+        int v = local, w = ltiles;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int n1 = __shfl_up_sync(0xffffffffu, v, o), n2 = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) { v += n1; w += n2; }
+        }
+        if (lane == 31) { s_wsum[warp] = v; s_wt[warp] = w; }
+        __syncthreads();
+        int base = 0, tbase = 0, tot = 0, ttot = 0;
+        for (int q = 0; q < MM_THREADS / 32; q++) {
+            if (q < warp) { base += s_wsum[q]; tbase += s_wt[q]; }
+            tot += s_wsum[q];
+            ttot += s_wt[q];
+        }
+        int pos = base + v - local, tpos = tbase + w - ltiles;
+#pragma unroll
+        for (int i = 0; i < PER; i++)
+            if (ne[i] > 0) { tbl[pos] = make_int4(tid * PER + i, tpos, eb[i], ne[i]); pos++; tpos += nt[i]; }
+        if (tid == 0) { s_nact = tot; s_total = ttot; }
+    }
+    g_fence_before();
+    __syncthreads();
+    if (CG == 2) g_cluster_sync();                   // the other CTA's barriers exist before anything arrives there
+    g_fence_after();
+
+    const uint32_t tmem = s_tmem;
+    const int ntiles = s_total, nact = s_nact;
+    const int tile0 = int(blockIdx.x) / CG, tstep = int(gridDim.x) / CG;
+    auto tile_of = [&](int tile) {
+        int lo = 0, hi = nact - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (tbl[mid].y <= tile) lo = mid; else hi = mid - 1;
+        }
+        const int4 te = tbl[lo];
+        MmTile t;
+        t.e = te.x;
+        const int local = tile - te.y, n_e = te.w;
+        const int ntile = (n_e + NT - 1) / NT;
+        const int per = (n_e + ntile - 1) / ntile;                 // balanced rows per tile
+        // the features of a row block run fastest: the CTAs of a wave share the rows, and the expert's
+        // weights stay in L2 from one row block to the next
+        const int n = local / MT;
+        t.m0 = (local - n * MT) * (128 * CG);
+        t.nval = min(per, n_e - n * per);
+        t.n0 = te.z + n * per;
+        t.bn = (t.nval + C::kStep - 1) / C::kStep * C::kStep;
+        return t;
+    };
+    auto fail = [&]() {
+        set_status(a.status, MOE_ERR_TIMEOUT);
+        s_ab.flag = 1;
+    };
+
+    if (warp == 0) {
+        // ---------------- producer (whole warp, one lane issues) ----------------
+        uint32_t it = 0;
+        bool ok = true;
+        bool rows_ready = !a.early;
+        for (int tile = tile0; tile < ntiles && ok && !g_aborted(&s_ab); tile += tstep) {
+            const MmTile T = tile_of(tile);
+            const int half = T.bn / CG;                            // rows of B this CTA stages
+            const int r0 = T.n0 + int(rank) * half;
+            const uint32_t bytes = uint32_t(C::kMat * C::kABytes + half * 128);
+            for (int ks = 0; ks < KS; ks++, it++) {
+                const int s = it % S;
+                if (it >= uint32_t(S) && !g_wait_w(g_smem(&empty[s]), ((it / S) - 1) & 1, &s_ab, 32)) {
+                    ok = false;
+                    break;
+                }
+                uint32_t bar = g_smem(&full[s]);
+                if (CG == 2) bar = g_mapa(bar, 0);                 // the pair's stages complete in its first CTA
+                const uint32_t sa = g_smem(ring + s * C::kStage), sb = sa + C::kMat * C::kABytes;
+                if (g_elect()) {
+                    if (CG == 2) g_expect_remote(bar, bytes); else g_expect(bar, bytes);
+                    const int m0 = T.m0 + int(rank) * 128;
+#pragma unroll
+                    for (int m = 0; m < C::kMat; m++) {
+                        const CUtensorMap* am = m ? &a.a1 : &a.a0;
+                        if constexpr (AMN) {
+                            for (int h = 0; h < 2; h++) {          // two halves of 64 features
+                                if (CG == 2) g_tma3d_pair(sa + m * C::kABytes + h * 8192, am, m0 + h * 64, ks * 64, T.e, bar);
+                                else g_tma3d(sa + m * C::kABytes + h * 8192, am, m0 + h * 64, ks * 64, T.e, bar);
+                            }
+                        } else {
+                            if (CG == 2) g_tma3d_pair(sa + m * C::kABytes, am, ks * C::kBK, m0, T.e, bar);
+                            else g_tma3d(sa + m * C::kABytes, am, ks * C::kBK, m0, T.e, bar);
+                        }
+                    }
+                }
+                __syncwarp();
+                if (!rows_ready) {                                 // the row pass's output, once
+                    asm volatile("griddepcontrol.wait;" ::: "memory");
+                    rows_ready = true;
+                }
+                if (g_elect()) {
+                    int r = 0;
+                    for (; r + 64 <= half; r += 64) {
+                        if (CG == 2) g_tma2d_pair(sb + r * 128, &a.b64, ks * C::kBK, r0 + r, bar);
+                        else g_tma2d(sb + r * 128, &a.b64, ks * C::kBK, r0 + r, bar);
+                    }
+                    for (; r < half; r += 16) {
+                        if (CG == 2) g_tma2d_pair(sb + r * 128, &a.b16, ks * C::kBK, r0 + r, bar);
+                        else g_tma2d(sb + r * 128, &a.b16, ks * C::kBK, r0 + r, bar);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        if (!rows_ready) asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (!ok) fail();
+        if (CG == 1) {
+            // every copy issued has landed before the CTA exits
+            if (lane == 0)
+                for (uint32_t n = it > uint32_t(S) ? it - S : 0; n < it; n++) g_drain_wait(g_smem(&full[n % S]), (n / S) & 1);
+        } else {
+            // the commits' arrivals here have landed too (the copies: see the end of the kernel)
+            if (lane == 0) {
+                s_issued = it;
+                if (!s_ab.flag)
+                    for (uint32_t n = it > uint32_t(S) ? it - S : 0; n < it; n++)
+                        if (!g_wait(g_smem(&empty[n % S]), (n / S) & 1, &s_ab)) { fail(); break; }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1 && rank == 0) {
+        // ---------------- MMA issuer (whole warp, one lane issues) ----------------
+        // failure testing (moe_set_wait_hold): wait for a barrier that nothing completes
+        if (s_hold && !g_wait_w(g_smem(&hold_bar), 0, &s_ab)) fail();
+        uint32_t it = 0;
+        int t = 0;
+        bool ok = true;
+        for (int tile = tile0; tile < ntiles && ok && !g_aborted(&s_ab); tile += tstep, t++) {
+            const MmTile T = tile_of(tile);
+            const uint32_t idesc = I8 ? g_idesc_s8(T.bn, 128 * CG)
+                                      : (g_idesc(T.bn, a.f16 != 0, 128 * CG) | (AMN ? G_IDESC_A_MN : 0u));
+            const uint32_t d = tmem + (t & 1) * C::kAccCols;
+            if (t >= 2 && !g_wait_w(g_smem(&acc_empty[t & 1]), ((t >> 1) - 1) & 1, &s_ab)) {
+                ok = false;
+                break;
+            }
+            g_fence_after();
+            for (int ks = 0; ks < KS; ks++, it++) {
+                const int s = it % S;
+                if (!g_wait_w(g_smem(&full[s]), (it / S) & 1, &s_ab)) {
+                    ok = false;
+                    break;
+                }
+                g_fence_after();
+                const uint32_t sa = g_smem(ring + s * C::kStage), sb = sa + C::kMat * C::kABytes;
+                if (g_elect()) {
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        const uint64_t bd = g_desc(sb + k * 32);
+                        const uint32_t acc = (k > 0 || ks > 0) ? 1u : 0u;
+#pragma unroll
+                        for (int m = 0; m < C::kMat; m++) {
+                            const uint32_t am = sa + m * C::kABytes;
+                            const uint64_t ad = AMN ? g_desc_mn(am + k * 2048, 8192) : g_desc(am + k * 32);
+                            if (I8) g_mma_s8<CG>(d + m * NT, ad, bd, idesc, acc);
+                            else g_mma_f16<CG>(d + m * NT, ad, bd, idesc, acc);
+                        }
+                    }
+                    g_commit_cg<CG>(g_smem(&empty[s]));
+                    if (ks == KS - 1) g_commit_cg<CG>(g_smem(&acc_full[t & 1]));
+                }
+                __syncwarp();
+            }
+        }
+        if (!ok) fail();
+        if (g_aborted(&s_ab)) {
+            // the MMAs issued so far have finished reading shared memory before the CTA exits
+            if (g_elect()) g_commit_own<CG>(g_smem(&drain));
+            __syncwarp();
+            if (lane == 0) g_drain_wait(g_smem(&drain), 0);
+            __syncwarp();
+        }
+    } else if (warp >= 4) {
+        // ---------------- epilogue ----------------
+        if (a.early) asm volatile("griddepcontrol.wait;" ::: "memory");      // the row pass's scales
+        const int q = warp & 3;
+        const uint32_t lane_addr = uint32_t(q * 32) << 16;
+        int t = 0;
+        bool ok = true;
+        for (int tile = tile0; tile < ntiles && !g_aborted(&s_ab); tile += tstep, t++) {
+            const MmTile T = tile_of(tile);
+            const int m = T.m0 + int(rank) * 128 + q * 32 + lane;            // my feature
+            const bool mine = m < a.mdim;
+            float w0 = 0.f, w1 = 0.f;
+            if (I8 && mine) {
+                w0 = a.s0[size_t(T.e) * a.mdim + m];
+                if (GU) w1 = a.s1[size_t(T.e) * a.mdim + m];
+            }
+            if (!g_wait_w(g_smem(&acc_full[t & 1]), (t >> 1) & 1, &s_ab, 32)) {
+                ok = false;
+                break;
+            }
+            g_fence_after();
+            const uint32_t acc = tmem + lane_addr + (t & 1) * C::kAccCols;
+            uint16_t* dst = a.out + size_t(T.n0) * a.mdim + m;
+            for (int c = 0; c < T.nval; c += 16) {
+                uint32_t v[16], u[16];
+                g_ld16(acc + c, v);
+                if constexpr (GU) g_ld16(acc + NT + c, u);
+                float rs = 0.f;                                               // lane j: the scale of row c + j
+                if (I8 && lane < 16 && c + lane < T.nval) {
+                    const int r = T.n0 + c + lane;
+                    rs = a.act_scale[r];
+                    if (!GU && a.topk_w) {
+                        const int slot = a.row_slot[r];
+                        if (slot >= 0 && slot < a.rows) rs *= a.topk_w[slot];
+                        else { set_status(a.status, MOE_ERR_DEVICE_INDEX); rs = 0.f; }
+                    }
+                }
+                g_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; j++) {
+                    float y;
+                    if constexpr (I8) {
+                        // the 32-bit sum is rounded to fp32 once (2^-24), then scaled
+                        const float f = __shfl_sync(0xffffffffu, rs, j);
+                        y = float(int32_t(v[j])) * (f * w0);
+                        if constexpr (GU) y = y / (1.0f + expf(-y)) * (float(int32_t(u[j])) * (f * w1));
+                    } else {
+                        y = __uint_as_float(v[j]);
+                    }
+                    if (mine && c + j < T.nval)
+                        dst[size_t(c + j) * a.mdim] = (!I8 && a.f16) ? __half_as_ushort(__float2half_rn(y))
+                                                                      : __bfloat16_as_ushort(__float2bfloat16_rn(y));
+                }
+            }
+            g_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                const uint32_t bar = g_smem(&acc_empty[t & 1]);
+                if (CG == 2) g_arrive_remote(g_mapa(bar, 0)); else g_arrive(bar);
+            }
+        }
+        if (!ok) fail();
+    }
+
+    g_fence_before();
+    __syncthreads();
+    if (CG == 2) {
+        g_cluster_sync();
+        // after an expired wait, copies may be in flight whose stage only one CTA had issued: stand in for the
+        // other's arrival, then wait (bounded) for the last stages of both
+        if (rank == 0 && tid == 0) {
+            const uint32_t p0 = s_issued, p1 = g_ld_cluster(g_mapa(g_smem(&s_issued), 1));
+            const uint32_t lo = min(p0, p1), hi = max(p0, p1);
+            for (uint32_t n = lo; n < hi; n++) g_arrive(g_smem(&full[n % S]));
+            for (uint32_t n = hi > uint32_t(S) ? hi - S : 0; n < hi; n++) g_drain_wait(g_smem(&full[n % S]), (n / S) & 1);
+        }
+    }
+    g_fence_after();
+    if (warp == 2) g_tmem_free<CG>(tmem, C::kTmem);
+    if (CG == 2) {
+        __syncwarp();
+        g_cluster_sync();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+template <bool I8, bool AMN, bool GU, int NT, int CG>
+static int mm_launch(const MmArgs& a, cudaStream_t s) {
+    using C = MmCfg<I8, AMN, GU, NT, CG>;
+    auto k = mm_kernel<I8, AMN, GU, NT, CG>;
+    constexpr int kSmem = C::kStages * C::kStage + 1024 + 16 * kMaxE;
+    int sms = 0;
+    const int rc = mm_kernel_ready(reinterpret_cast<const void*>(k), kSmem, &sms);
+    if (rc != MOE_OK) return rc;
+    const int smem = C::kStages * C::kStage + 1024 + 16 * a.E;
+    return mm_launch_cfg(k, dim3(sms / CG * CG), dim3(MM_THREADS), smem, CG, s, a);
+}
+
+static CUtensorMapDataType mm_type(bool i8, bool f16) {
+    return i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : (f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
+}
+
+int launch_grouped_mm(const MmProblem& p, cudaStream_t s) {
+    if (p.rows <= 0) return MOE_OK;
+    const int ge = g_encoder();
+    if (ge != MOE_OK) return ge;
+    MmArgs a;
+    memset(&a, 0, sizeof(a));
+    const int el = p.i8 ? 1 : 2, bk = 128 / el;
+    const CUtensorMapDataType ty = mm_type(p.i8, p.f16);
+    // weights [E][out][in]: boxes of 128 features x 128 bytes of K, or (gradient) 64 features of `in` x 64 of K
+    const uint64_t pitch = uint64_t(p.in_dim) * el, zp = pitch * p.out_dim;
+    const uint32_t bi = p.grad ? 64 : bk, br = p.grad ? 64 : 128;
+    int rc = g_map3(&a.a0, ty, p.w0, p.in_dim, p.out_dim, p.E, pitch, zp, bi, br);
+    if (rc == MOE_OK && p.w1) rc = g_map3(&a.a1, ty, p.w1, p.in_dim, p.out_dim, p.E, pitch, zp, bi, br);
+    const int kdim = p.grad ? p.out_dim : p.in_dim;
+    if (rc == MOE_OK) rc = g_map(&a.b16, !p.i8, p.act, kdim, p.rows, uint64_t(kdim) * el, bk, 16, true);
+    if (rc == MOE_OK) rc = g_map(&a.b64, !p.i8, p.act, kdim, p.rows, uint64_t(kdim) * el, bk, 64, true);
+    if (rc != MOE_OK) return rc;
+    a.offsets = p.offsets;
+    a.row_slot = p.row_slot;
+    a.topk_w = p.topk_w;
+    a.act_scale = p.act_scale;
+    a.s0 = p.s0;
+    a.s1 = p.s1;
+    a.out = p.out;
+    a.status = p.status;
+    a.E = p.E;
+    a.mdim = p.grad ? p.in_dim : p.out_dim;
+    a.kdim = kdim;
+    a.rows = p.rows;
+    a.f16 = p.f16;
+    a.early = p.i8;
+    const bool few = p.rows <= 16 * p.E;
+    if (p.i8) {
+        if (p.w1) return few ? mm_launch<true, false, true, 16, 1>(a, s) : mm_launch<true, false, true, 128, 1>(a, s);
+        return few ? mm_launch<true, false, false, 16, 1>(a, s) : mm_launch<true, false, false, 256, 1>(a, s);
+    }
+    if (p.grad) return few ? mm_launch<false, true, false, 16, 1>(a, s) : mm_launch<false, true, false, 256, 1>(a, s);
+    return few ? mm_launch<false, false, false, 16, 1>(a, s) : mm_launch<false, false, false, 256, 1>(a, s);
+}
+
+}  // namespace moe

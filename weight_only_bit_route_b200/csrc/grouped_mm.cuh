@@ -1,0 +1,75 @@
+// Internal declarations of the expert products in 16 and 8 bits (grouped_mm.cu, grouped_wgrad.cu, quant_int8.cu).
+#pragma once
+
+#include "moe_internal.cuh"
+
+namespace moe {
+
+// The rows of expert e: [base, base + n).  Offsets outside [0, rows] or decreasing are clipped and recorded, so
+// that no index derived from them leaves the rows.
+__device__ __forceinline__ void mm_expert_rows(const int32_t* offsets, int e, int rows, int32_t* status, int& base,
+                                               int& n) {
+    const int o0 = offsets[e], o1 = offsets[e + 1];
+    base = min(max(o0, 0), rows);
+    const int end = min(max(o1, base), rows);
+    n = end - base;
+    if (base != o0 || end != o1) set_status(status, MOE_ERR_DEVICE_INDEX);
+}
+
+struct MmProblem {
+    const void* act;             // rows of the contraction: x or codes [rows, in], dy [rows, out] (grad)
+    const void* w0; const void* w1;      // weights [E, out, in]; w1: up (int8 gate/up), else null
+    const float* s0; const float* s1;    // int8: channel scales [E, out]
+    const float* act_scale;              // int8: row scales [rows]
+    const int32_t* offsets;              // [E + 1]
+    const int32_t* row_slot;             // int8: [rows], for topk_w
+    const float* topk_w;                 // int8: weight by slot, nullable
+    uint16_t* out;                       // [rows, out], [rows, in] (grad)
+    int32_t* status;
+    int E, out_dim, in_dim, rows;
+    bool i8, f16, grad;
+};
+int launch_grouped_mm(const MmProblem& p, cudaStream_t s);
+
+struct WgradProblem {
+    const void* dy; const void* x;       // [rows, out], [rows, in]
+    const int32_t* offsets;
+    void* dw;                            // [E, out, in], 16 bits or fp32
+    int32_t* status;
+    int E, out_dim, in_dim, rows;
+    bool f16, out_f32, accumulate;
+};
+int launch_grouped_wgrad(const WgradProblem& p, cudaStream_t s);
+
+// Rows to 8 bits: codes [rows, cols], scales [rows].  With row_slot, row r reads row row_slot[r] / top_k of the
+// nsrc rows of x; with nrows (device), rows from *nrows on are left alone.  status nullable.
+int launch_quant_int8(const void* x, bool f16, int64_t rows, int64_t cols, const int32_t* row_slot, int top_k,
+                      int64_t nsrc, const int32_t* nrows, int8_t* codes, float* scales, int32_t* status,
+                      cudaStream_t s);
+
+// One-time set-up of a kernel on the current device: its shared-memory attribute; *sms: the device's SM count.
+int mm_kernel_ready(const void* kernel, int smem_bytes, int* sms);
+
+// Launch with programmatic dependent launch allowed, in clusters of `cluster` CTAs.
+template <typename K, typename... Args>
+inline int mm_launch_cfg(K kern, dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t s, const Args&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) return MOE_ERR_CUDA;
+    count_launch();
+    return MOE_OK;
+}
+
+}  // namespace moe

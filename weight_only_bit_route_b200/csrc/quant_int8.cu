@@ -1,0 +1,143 @@
+// Rows to 8-bit integers with a scale for each row:
+//     s = max|x| / 127 (fp32),  q = rint(127 x / max|x|), ties to even, in [-127, 127]
+// A zero row gets s = 0 and zero codes.  A row that holds an infinity or a NaN gets s = NaN and zero codes, so
+// that every product of the row is NaN.
+//
+// The codes are those of the real quotient: 127 x has at most 18 significant bits, so a quotient that is no tie
+// lies at least 2^-21 of its size away from one, further than fp32 rounds; the division in fp32 (IEEE) then
+// rounds to the same side, and a tie is exact.  The kernel multiplies by 127 / max|x| first (within 2^-16 of
+// the quotient) and divides only where that lands within 2^-12 of a tie.
+//
+// One block per row, the row's first 4096 elements kept in registers between the two passes.  Bound by the
+// row's bytes: 2 read and 1 written per element.
+#include <mutex>
+
+#include "grouped_mm.cuh"
+
+namespace moe {
+
+constexpr int Q8_THREADS = 128;
+constexpr int Q8_KEEP = 4;               // 16-byte chunks per thread kept in registers
+
+// max of the 16-bit magnitudes (sign dropped): as unsigned numbers they order like the values, infinity and NaN last
+__device__ __forceinline__ uint32_t q8_max2(uint32_t m, uint32_t v) { return __vmaxu2(m, v & 0x7fff7fffu); }
+__device__ __forceinline__ uint32_t q8_max8(uint32_t m, const uint4& v) {
+    return q8_max2(q8_max2(q8_max2(q8_max2(m, v.x), v.y), v.z), v.w);
+}
+
+__device__ __forceinline__ int q8_code(float x, float r, float amax, bool slow) {
+    const float t = x * r;
+    float k = rintf(t);
+    if (slow || fabsf(t - k) > 0.5f - 0x1p-12f) {
+        // near a tie, or a row so small that 127 / amax overflows.  Powers of two keep 127 x in range.
+        const float c = amax > 0x1p100f ? 0x1p-16f : (amax < 0x1p-90f ? 0x1p64f : 1.f);
+        k = rintf(__fdiv_rn(127.f * (x * c), amax * c));
+    }
+    return int(k);
+}
+
+template <bool F16>
+__global__ void __launch_bounds__(Q8_THREADS) quant_int8_kernel(const uint16_t* __restrict__ x, long long cols,
+                                                               const int32_t* __restrict__ row_slot, int top_k,
+                                                               long long nsrc, const int32_t* __restrict__ nrows,
+                                                               int8_t* __restrict__ codes, float* __restrict__ scales,
+                                                               int32_t* status) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the product's weights need nothing from here
+    const long long row = blockIdx.x;
+    if (nrows && row >= *nrows) return;                               // behind the last expert's rows
+    long long src = row;
+    if (row_slot) {
+        src = row_slot[row] / top_k;
+        if (row_slot[row] < 0 || src >= nsrc) {
+            if (threadIdx.x == 0) {
+                if (status) set_status(status, MOE_ERR_DEVICE_INDEX);
+                scales[row] = 0.f;
+            }
+            src = -1;
+        }
+    }
+    const long long n = cols / 8;
+    uint2* dst = reinterpret_cast<uint2*>(codes + row * cols);
+    if (src < 0) {
+        for (long long i = threadIdx.x; i < n; i += Q8_THREADS) dst[i] = make_uint2(0, 0);
+        return;
+    }
+    const uint4* p = reinterpret_cast<const uint4*>(x + src * cols);
+    uint4 keep[Q8_KEEP];
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < Q8_KEEP; j++) {
+        const long long i = threadIdx.x + j * Q8_THREADS;
+        keep[j] = i < n ? p[i] : make_uint4(0, 0, 0, 0);
+        m = q8_max8(m, keep[j]);
+    }
+    for (long long i = threadIdx.x + Q8_KEEP * Q8_THREADS; i < n; i += Q8_THREADS) m = q8_max8(m, p[i]);
+    for (int o = 16; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    __shared__ uint32_t sm[Q8_THREADS / 32];
+    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < Q8_THREADS / 32; w++) m = __vmaxu2(m, sm[w]);
+    m = max(m & 0xffffu, m >> 16);
+    const bool bad = m >= (F16 ? 0x7c00u : 0x7f80u);
+    const float amax = act_lo<F16>(m);
+    if (threadIdx.x == 0) {
+        scales[row] = bad ? __int_as_float(0x7fffffff) : __fdiv_rn(amax, 127.f);
+        if (bad && status) set_status(status, MOE_ERR_NONFINITE);
+    }
+    const bool zero = bad || m == 0;
+    const float r = __fdiv_rn(127.f, amax);
+    const bool slow = amax < 0x1p-90f;
+    auto put = [&](long long i, const uint4& v) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t o[2] = {0, 0};
+        if (!zero) {
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const int lo = q8_code(act_lo<F16>(w[j]), r, amax, slow), hi = q8_code(act_hi<F16>(w[j]), r, amax, slow);
+                o[j >> 1] |= ((uint32_t(lo) & 0xffu) | ((uint32_t(hi) & 0xffu) << 8)) << (16 * (j & 1));
+            }
+        }
+        dst[i] = make_uint2(o[0], o[1]);
+    };
+#pragma unroll
+    for (int j = 0; j < Q8_KEEP; j++) {
+        const long long i = threadIdx.x + j * Q8_THREADS;
+        if (i < n) put(i, keep[j]);
+    }
+    for (long long i = threadIdx.x + Q8_KEEP * Q8_THREADS; i < n; i += Q8_THREADS) put(i, p[i]);
+}
+
+int launch_quant_int8(const void* x, bool f16, int64_t rows, int64_t cols, const int32_t* row_slot, int top_k,
+                      int64_t nsrc, const int32_t* nrows, int8_t* codes, float* scales, int32_t* status,
+                      cudaStream_t s) {
+    if (rows <= 0) return MOE_OK;
+    auto k = f16 ? quant_int8_kernel<true> : quant_int8_kernel<false>;
+    return mm_launch_cfg(k, dim3(unsigned(rows)), dim3(Q8_THREADS), 0, 1, s, static_cast<const uint16_t*>(x),
+                         (long long)cols, row_slot, top_k, (long long)nsrc, nrows, codes, scales, status);
+}
+
+// Per device and kernel: the shared-memory attribute, set once under a lock.
+int mm_kernel_ready(const void* kernel, int smem_bytes, int* sms) {
+    struct Dev { int sms = 0; int n = 0; const void* ready[32] = {}; };
+    static std::mutex mu;
+    static Dev devs[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MOE_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(mu);
+    Dev& d = devs[dev];
+    if (!d.sms && cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        d.sms = 0;
+        return MOE_ERR_CUDA;
+    }
+    *sms = d.sms;
+    for (int i = 0; i < d.n; i++)
+        if (d.ready[i] == kernel) return MOE_OK;
+    if (d.n == 32 || cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    d.ready[d.n++] = kernel;
+    return MOE_OK;
+}
+
+}  // namespace moe

@@ -20,7 +20,7 @@ if not os.path.exists(LIB_PATH):
 
 lib = ctypes.CDLL(LIB_PATH)
 
-FMT_INT4_G128, FMT_NVFP4, FMT_BF16 = 0, 1, 2
+FMT_INT4_G128, FMT_NVFP4, FMT_BF16, FMT_INT8 = 0, 1, 2, 5
 STATUS = {0: "MOE_OK", -1: "MOE_ERR_INVALID_ARG", -2: "MOE_ERR_UNSUPPORTED", -3: "MOE_ERR_CUDA",
           -4: "MOE_ERR_TIMEOUT", -5: "MOE_ERR_WORKSPACE", -6: "MOE_ERR_DEVICE_INDEX", -7: "MOE_ERR_NONFINITE"}
 
@@ -64,6 +64,9 @@ _sig("moe_permute", _I, [_P, _I, _I, _I, _P, _P, _P, _P, _SZ, _P])
 _sig("moe_permute_noalloc", _I, [_P, _I, _I, _I, _P, _P, _P, _P])
 _sig("moe_grouped_w4a16_swiglu", _I, [_P, _I, _I, _P, _P, _I, _P, _P, _F, _P, _P, _SZ, _P])
 _sig("moe_grouped_w4a16_down", _I, [_P, _P, _P, _P, _I, _P, _P, _P, _SZ, _P])
+_sig("moe_grouped_mm", _I, [_P, _P, _I, _P, _I, _I, _I, _I, _P, _P, _SZ, _P])
+_sig("moe_grouped_mm_dgrad", _I, [_P, _P, _I, _P, _I, _I, _I, _I, _P, _P, _SZ, _P])
+_sig("moe_grouped_mm_wgrad", _I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _I, _I, _P, _SZ, _P])
 _sig("moe_unpermute_combine", _I, [_P, _P, _I, _I, _I, _P, _P, _P])
 _sig("moe_layer_decode", _I, [_P, _I, _P, _P, _P, _SZ, _P])
 _sig("moe_layer_forward", _I, [_P, _I, _P, _P, _P, _SZ, _P])
@@ -71,6 +74,7 @@ _sig("moe_layer_graph_create", _I, [_P, _I, _P, _P, _P, _SZ, ctypes.POINTER(_P)]
 _sig("moe_layer_graph_launch", _I, [_P, _P])
 _sig("moe_layer_graph_destroy", _I, [_P])
 _sig("moe_quantize_int4_g128", _I, [_P, _I64, _I64, _P, _P, _P])
+_sig("moe_quantize_int8", _I, [_P, _I64, _I64, _I, _P, _P, _P])
 _sig("moe_quantize_nvfp4", _I, [_P, _I64, _I64, _P, _P, _P, _P, _SZ, _P])
 _sig("moe_quantize_nvfp4_act", _I, [_P, _I64, _I64, _P, _P, _P, _P])
 _sig("moe_csf_decode", _I, [_P, _P, _P, _I, _I, _I, _P, _P, _P])
@@ -110,6 +114,7 @@ class Bank:
     int4:  packed int32 [E,out,in/8], scales bf16 [E,out,in/128]
     nvfp4: packed uint8 [E,out,in/2], scales uint8 [E,out,in/16], global_scale fp32 [E]
     bf16:  packed bf16 [E,out,in]
+    int8:  packed int8 [E,out,in], scales fp32 [E,out]
     """
 
     def __init__(self, fmt, packed, scales=None, global_scale=None, out_dim=None, in_dim=None, input_scale=None):
@@ -117,7 +122,7 @@ class Bank:
         self.input_scale = input_scale       # NVFP4 W4A4: activation global scale by expert, fp32 [E]
         self.E = packed.shape[0]
         self.out_dim = packed.shape[1] if out_dim is None else out_dim
-        mult = {FMT_INT4_G128: 8, FMT_NVFP4: 2, FMT_BF16: 1}[fmt]
+        mult = {FMT_INT4_G128: 8, FMT_NVFP4: 2, FMT_BF16: 1, FMT_INT8: 1}[fmt]
         self.in_dim = packed.shape[2] * mult if in_dim is None else in_dim
 
     def struct(self):
@@ -159,6 +164,13 @@ def workspace(T, H, E, F, top_k, device="cuda"):
         raise MoEError("moe_workspace_bytes", -2)
     ws = torch.empty(n, dtype=torch.uint8, device=device)
     _check("moe_workspace_init", lib.moe_workspace_init(_ptr(ws), n, _stream()))
+    return ws
+
+
+def control_block(device="cuda"):
+    """A workspace for the calls that need no more than the control block (the 16-bit products)."""
+    ws = torch.empty(1024, dtype=torch.uint8, device=device)
+    _check("moe_workspace_init", lib.moe_workspace_init(_ptr(ws), 1024, _stream()))
     return ws
 
 
@@ -235,6 +247,80 @@ def grouped_down(h_perm, offsets, row_slot, topk_w, down, ws, out=None):
     return y
 
 
+def _need(fn, ok, what):
+    if not ok:
+        raise MoEError(f"{fn}: {what}", -1)
+
+
+def _mm_args(fn, offsets, ws, **tensors):
+    """Checks what the C entry cannot see: types, shapes' agreement, contiguity, one device."""
+    ts = list(tensors.values())
+    dt, dev = ts[0].dtype, ts[0].device
+    _need(fn, dt in (torch.bfloat16, torch.float16), "bf16 or fp16 tensors")
+    for name, t in tensors.items():
+        _need(fn, t.dtype == dt, f"{name} has another type")
+    for name, t in dict(tensors, offsets=offsets, ws=ws).items():
+        _need(fn, t.device == dev and t.is_cuda, f"{name} is not on the tensors' CUDA device")
+        _need(fn, t.is_contiguous(), f"{name} is not contiguous")
+    _need(fn, offsets.dtype == torch.int32 and offsets.dim() == 1 and offsets.numel() >= 2, "offsets: int32 [E+1]")
+    return offsets.numel() - 1, int(dt == torch.float16)
+
+
+def _mm_out(fn, out, shape, dtype, like):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _need(fn, tuple(out.shape) == tuple(shape) and out.dtype == dtype and out.device == like.device
+          and out.is_contiguous(), f"out must be contiguous {dtype} {tuple(shape)} on the tensors' device")
+    return out
+
+
+def grouped_mm(x, w, offsets, ws, out=None):
+    """y[r] = w[e] x[r] for the rows r of each expert e (bf16 or fp16): x [rows, in], w [E, out, in] -> [rows, out].
+    Rows outside every expert are not written."""
+    fn = "moe_grouped_mm"
+    E, f16 = _mm_args(fn, offsets, ws, x=x, w=w)
+    _need(fn, x.dim() == 2 and w.dim() == 3 and w.shape[0] == E and w.shape[2] == x.shape[1],
+          "x [rows, in], w [E, out, in]")
+    rows, (_, n_out, n_in) = x.shape[0], w.shape
+    y = _mm_out(fn, out, (rows, n_out), x.dtype, x)
+    with torch.cuda.device(x.device):
+        _check(fn, lib.moe_grouped_mm(_ptr(x), _ptr(offsets), rows, _ptr(w), E, n_out, n_in, f16, _ptr(y), _ptr(ws),
+                                      ws.numel(), _stream()))
+    return y
+
+
+def grouped_mm_dgrad(dy, w, offsets, ws, out=None):
+    """Gradient of grouped_mm by x: dx[r] = w[e]^T dy[r]; dy [rows, out], w [E, out, in] -> [rows, in]."""
+    fn = "moe_grouped_mm_dgrad"
+    E, f16 = _mm_args(fn, offsets, ws, dy=dy, w=w)
+    _need(fn, dy.dim() == 2 and w.dim() == 3 and w.shape[0] == E and w.shape[1] == dy.shape[1],
+          "dy [rows, out], w [E, out, in]")
+    rows, (_, n_out, n_in) = dy.shape[0], w.shape
+    dx = _mm_out(fn, out, (rows, n_in), dy.dtype, dy)
+    with torch.cuda.device(dy.device):
+        _check(fn, lib.moe_grouped_mm_dgrad(_ptr(dy), _ptr(offsets), rows, _ptr(w), E, n_out, n_in, f16, _ptr(dx),
+                                            _ptr(ws), ws.numel(), _stream()))
+    return dx
+
+
+def grouped_mm_wgrad(dy, x, offsets, ws, out=None, out_dtype=None, accumulate=False):
+    """Gradient of grouped_mm by w: dw[e] = sum over e's rows of dy[r] x[r]^T -> [E, out, in], in the tensors'
+    type or fp32.  accumulate: add to `out` (fp32) instead."""
+    fn = "moe_grouped_mm_wgrad"
+    E, f16 = _mm_args(fn, offsets, ws, dy=dy, x=x)
+    _need(fn, dy.dim() == 2 and x.dim() == 2 and dy.shape[0] == x.shape[0], "dy [rows, out], x [rows, in]")
+    dt = out_dtype or (out.dtype if out is not None else dy.dtype)
+    _need(fn, dt in (dy.dtype, torch.float32), "out_dtype: the tensors' type or float32")
+    _need(fn, not accumulate or out is not None, "accumulate needs out")
+    rows, n_out, n_in = dy.shape[0], dy.shape[1], x.shape[1]
+    dw = _mm_out(fn, out, (E, n_out, n_in), dt, dy)
+    with torch.cuda.device(dy.device):
+        _check(fn, lib.moe_grouped_mm_wgrad(_ptr(dy), _ptr(x), _ptr(offsets), rows, E, n_out, n_in, f16, _ptr(dw),
+                                            int(dt == torch.float32), int(bool(accumulate)), _ptr(ws), ws.numel(),
+                                            _stream()))
+    return dw
+
+
 def unpermute_combine(y_perm, slot_row, T, top_k, shared_out=None, out=None):
     H = y_perm.shape[1]
     y = out if out is not None else torch.empty(T, H, dtype=torch.bfloat16, device=y_perm.device)
@@ -299,6 +385,20 @@ def quantize_int4_g128(w):
     _check("moe_quantize_int4_g128",
            lib.moe_quantize_int4_g128(_ptr(w), rows, cols, _ptr(packed), _ptr(scales), _stream()))
     return packed, scales
+
+
+def quantize_int8(x):
+    """Rows of x (bf16 or fp16 [rows, cols]) -> (codes int8 [rows, cols], scales fp32 [rows])."""
+    fn = "moe_quantize_int8"
+    _need(fn, x.dim() == 2 and x.dtype in (torch.bfloat16, torch.float16) and x.is_cuda and x.is_contiguous(),
+          "x: contiguous bf16 or fp16 [rows, cols] on a CUDA device")
+    rows, cols = x.shape
+    codes = torch.empty(rows, cols, dtype=torch.int8, device=x.device)
+    scales = torch.empty(rows, dtype=torch.float32, device=x.device)
+    with torch.cuda.device(x.device):
+        _check(fn, lib.moe_quantize_int8(_ptr(x), rows, cols, int(x.dtype == torch.float16), _ptr(codes),
+                                         _ptr(scales), _stream()))
+    return codes, scales
 
 
 def quantize_nvfp4(w, ws, global_out=None):
