@@ -15,8 +15,8 @@
 // A tile is (expert, 128 * CG features, up to NT rows).  A persistent CTA (or pair) takes every grid-th tile;
 // every role computes the same sequence from a table of the experts' first tiles in shared memory, so nothing is
 // handed out through the workspace.  Warp roles:
-//   warp 0     TMA producer.  A stage is K = 128 bytes (64 elements of 16 bits, 128 of 8) of A and B, 128-byte
-//              swizzled; rows past the tensors' ends arrive as zeros, and so does K past its end on both sides.
+//   warps 0, 3 TMA producers of A and B.  A stage is SL slices of K = 128 bytes (64 elements of 16 bits, 128 of 8)
+//              of A and B, 128-byte swizzled; rows past the tensors' ends arrive as zeros, and so does K past its end on both sides.
 //   warp 1     issues the MMAs (in a pair: the first CTA's warp, for both) and commits each stage.
 //   warps 4-7  epilogue from tensor memory: lane = feature, column = row.  Two accumulator buffers, so that the
 //              epilogue of a tile overlaps the next tile's products.
@@ -32,14 +32,16 @@
 namespace moe {
 
 constexpr int MM_THREADS = 256;
+constexpr int MM_BOXES = 4;
 
-// Tile shape of one instantiation.  NT: rows per tile; CG: CTAs per tile.
-template <bool I8, bool AMN, bool GU, int NT, int CG>
+// Tile shape of one instantiation.  NT: rows per tile; CG: CTAs per tile; SL: 128-byte slices of K per stage.
+template <bool I8, bool AMN, bool GU, int NT, int CG, int SL>
 struct MmCfg {
     static constexpr int kMat = GU ? 2 : 1;
-    static constexpr int kBK = I8 ? 128 : 64;                     // K per stage (128 bytes)
-    static constexpr int kABytes = 128 * 128;                     // per matrix
-    static constexpr int kBBytes = NT / CG * 128;
+    static constexpr int kBK = (I8 ? 128 : 64) * SL;              // K per stage
+    static constexpr int kMmaK = I8 ? 32 : 16;                    // K per MMA
+    static constexpr int kABytes = SL * 128 * 128;                // per matrix
+    static constexpr int kBBytes = SL * NT / CG * 128;
     static constexpr int kStage = kMat * kABytes + kBBytes;
     static constexpr int kRingBytes = 200 * 1024;                 // beside it: the tile table (16 bytes per expert)
     static constexpr int kStages = kRingBytes / kStage < 12 ? kRingBytes / kStage : 12;
@@ -47,13 +49,14 @@ struct MmCfg {
     static constexpr int kTmem = 2 * kAccCols <= 32 ? 32 : (2 * kAccCols <= 64 ? 64 : (2 * kAccCols <= 128 ? 128 : (2 * kAccCols <= 256 ? 256 : 512)));
     static constexpr int kStep = 16 * CG;                         // a tile's N is a multiple of this
     static_assert(2 * kAccCols <= 512 && NT % kStep == 0 && kStages >= 2, "tile shape");
+    static_assert(NT / CG <= (16 << (MM_BOXES - 1)), "the largest box holds a tile's rows");
 };
 
 struct MmTile { int e, m0, n0, nval, bn; };                       // n0: first row (of all rows)
 
 struct MmArgs {
     CUtensorMap a0, a1;                  // weights [E][out][in]; a1: up (gate/up)
-    CUtensorMap b16, b64;                // rows, boxes of 16 and 64
+    CUtensorMap b[MM_BOXES];             // rows, boxes of 16, 32, 64 and 128
     const int32_t* offsets;
     const int32_t* row_slot;             // int8: slot of a row (routing weight), nullable
     const float* topk_w;
@@ -63,17 +66,31 @@ struct MmArgs {
     int32_t* status;
     int E, mdim, kdim, rows;             // mdim: output features (A's M), kdim: contraction length
     int f16;                             // 16-bit elements are fp16 (else bf16)
+    int chunked;                         // bit 0: a0 and a1, bit 1: b see K (gradient: A's features) in 128-byte chunks
     int early;                           // the kernel before is this product's own row pass
 };
 
-template <bool I8, bool AMN, bool GU, int NT, int CG>
+template <int CG>
+__device__ __forceinline__ void mm_copy2(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    if (CG == 2) g_tma2d_pair(dst, map, x, y, bar); else g_tma2d(dst, map, x, y, bar);
+}
+template <int CG>
+__device__ __forceinline__ void mm_copy3(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    if (CG == 2) g_tma3d_pair(dst, map, x, y, z, bar); else g_tma3d(dst, map, x, y, z, bar);
+}
+template <int CG>
+__device__ __forceinline__ void mm_copy4(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
+    if (CG == 2) g_tma4d_pair(dst, map, x, y, z, w, bar); else g_tma4d(dst, map, x, y, z, w, bar);
+}
+
+template <bool I8, bool AMN, bool GU, int NT, int CG, int SL>
 __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant__ MmArgs a) {
-    using C = MmCfg<I8, AMN, GU, NT, CG>;
+    using C = MmCfg<I8, AMN, GU, NT, CG, SL>;
     constexpr int S = C::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ __align__(8) uint64_t full[S], empty[S], acc_full[2], acc_empty[2], drain, hold_bar;
     __shared__ uint32_t s_tmem;
-    __shared__ uint32_t s_issued;                    // stages this CTA's producer has issued
+    __shared__ uint32_t s_issued[2];                 // stages this CTA's two producers have issued
     __shared__ int s_wsum[MM_THREADS / 32], s_wt[MM_THREADS / 32], s_nact, s_total, s_hold;
     __shared__ volatile GAbort s_ab;
 
@@ -84,7 +101,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
 
     if (tid == 0) {
         for (int s = 0; s < S; s++) {
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(g_smem(&full[s])), "r"(CG));
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(g_smem(&full[s])), "r"(2 * CG));
             asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(g_smem(&empty[s])));
         }
         for (int s = 0; s < 2; s++) {
@@ -95,7 +112,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
         asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(g_smem(&hold_bar)));
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         s_ab.flag = 0;
-        s_issued = 0;
+        s_issued[0] = s_issued[1] = 0;
     }
     if (warp == 2) g_tmem_alloc<CG>(g_smem(&s_tmem), C::kTmem);
     if (!a.early) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -172,16 +189,21 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
         s_ab.flag = 1;
     };
 
-    if (warp == 0) {
-        // ---------------- producer (whole warp, one lane issues) ----------------
+    if (warp == 0 || warp == 3) {
+        // ---------------- producers of A (warp 0) and B (warp 3); one lane issues ----------------
+        // Two warps, since a copy costs its issuer about 80 cycles and each stage some 100 more.
+        const bool isb = warp == 3;
+        if (isb && a.early) asm volatile("griddepcontrol.wait;" ::: "memory");      // the row pass's output
         uint32_t it = 0;
         bool ok = true;
-        bool rows_ready = !a.early;
         for (int tile = tile0; tile < ntiles && ok && !g_aborted(&s_ab); tile += tstep) {
             const MmTile T = tile_of(tile);
             const int half = T.bn / CG;                            // rows of B this CTA stages
-            const int r0 = T.n0 + int(rank) * half;
-            const uint32_t bytes = uint32_t(C::kMat * C::kABytes + half * 128);
+            // the smallest box that holds them (the rows too many are never multiplied)
+            const int bx = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
+            const uint32_t slice = uint32_t(16 << bx) * 128u;
+            const uint32_t bytes = isb ? SL * slice : uint32_t(C::kMat * C::kABytes);
+            const int r0 = T.n0 + int(rank) * half, m0 = T.m0 + int(rank) * 128;
             for (int ks = 0; ks < KS; ks++, it++) {
                 const int s = it % S;
                 if (it >= uint32_t(S) && !g_wait_w(g_smem(&empty[s]), ((it / S) - 1) & 1, &s_ab, 32)) {
@@ -193,54 +215,48 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
                 const uint32_t sa = g_smem(ring + s * C::kStage), sb = sa + C::kMat * C::kABytes;
                 if (g_elect()) {
                     if (CG == 2) g_expect_remote(bar, bytes); else g_expect(bar, bytes);
-                    const int m0 = T.m0 + int(rank) * 128;
-#pragma unroll
-                    for (int m = 0; m < C::kMat; m++) {
-                        const CUtensorMap* am = m ? &a.a1 : &a.a0;
-                        if constexpr (AMN) {
-                            for (int h = 0; h < 2; h++) {          // two halves of 64 features
-                                if (CG == 2) g_tma3d_pair(sa + m * C::kABytes + h * 8192, am, m0 + h * 64, ks * 64, T.e, bar);
-                                else g_tma3d(sa + m * C::kABytes + h * 8192, am, m0 + h * 64, ks * 64, T.e, bar);
-                            }
+                    if (isb) {
+                        if (SL == 1) {
+                            mm_copy2<CG>(sb, &a.b[bx], ks * C::kBK, r0, bar);
+                        } else if (a.chunked & 2) {
+                            mm_copy4<CG>(sb, &a.b[bx], 0, r0, ks * SL, 0, bar);
                         } else {
-                            if (CG == 2) g_tma3d_pair(sa + m * C::kABytes, am, ks * C::kBK, m0, T.e, bar);
-                            else g_tma3d(sa + m * C::kABytes, am, ks * C::kBK, m0, T.e, bar);
+                            for (int l = 0; l < SL; l++)
+                                mm_copy2<CG>(sb + l * slice, &a.b[bx], ks * C::kBK + l * (C::kBK / SL), r0, bar);
                         }
-                    }
-                }
-                __syncwarp();
-                if (!rows_ready) {                                 // the row pass's output, once
-                    asm volatile("griddepcontrol.wait;" ::: "memory");
-                    rows_ready = true;
-                }
-                if (g_elect()) {
-                    int r = 0;
-                    for (; r + 64 <= half; r += 64) {
-                        if (CG == 2) g_tma2d_pair(sb + r * 128, &a.b64, ks * C::kBK, r0 + r, bar);
-                        else g_tma2d(sb + r * 128, &a.b64, ks * C::kBK, r0 + r, bar);
-                    }
-                    for (; r < half; r += 16) {
-                        if (CG == 2) g_tma2d_pair(sb + r * 128, &a.b16, ks * C::kBK, r0 + r, bar);
-                        else g_tma2d(sb + r * 128, &a.b16, ks * C::kBK, r0 + r, bar);
+                    } else {
+#pragma unroll
+                        for (int m = 0; m < C::kMat; m++) {
+                            const CUtensorMap* am = m ? &a.a1 : &a.a0;
+                            const uint32_t d = sa + m * C::kABytes;
+                            if constexpr (AMN) {                   // two halves of 64 features, SL * 64 rows each
+                                if (a.chunked & 1) {
+                                    mm_copy4<CG>(d, am, 0, ks * C::kBK, m0 / 64, T.e, bar);
+                                } else {
+                                    for (int h = 0; h < 2; h++)
+                                        mm_copy3<CG>(d + h * (SL * 8192), am, m0 + h * 64, ks * C::kBK, T.e, bar);
+                                }
+                            } else if (SL == 1) {
+                                mm_copy3<CG>(d, am, ks * C::kBK, m0, T.e, bar);
+                            } else if (a.chunked & 1) {
+                                mm_copy4<CG>(d, am, 0, m0, ks * SL, T.e, bar);
+                            } else {
+                                for (int l = 0; l < SL; l++)
+                                    mm_copy3<CG>(d + l * 16384, am, ks * C::kBK + l * (C::kBK / SL), m0, T.e, bar);
+                            }
+                        }
                     }
                 }
                 __syncwarp();
             }
         }
-        if (!rows_ready) asm volatile("griddepcontrol.wait;" ::: "memory");
         if (!ok) fail();
-        if (CG == 1) {
-            // every copy issued has landed before the CTA exits
-            if (lane == 0)
-                for (uint32_t n = it > uint32_t(S) ? it - S : 0; n < it; n++) g_drain_wait(g_smem(&full[n % S]), (n / S) & 1);
-        } else {
-            // the commits' arrivals here have landed too (the copies: see the end of the kernel)
-            if (lane == 0) {
-                s_issued = it;
-                if (!s_ab.flag)
-                    for (uint32_t n = it > uint32_t(S) ? it - S : 0; n < it; n++)
-                        if (!g_wait(g_smem(&empty[n % S]), (n / S) & 1, &s_ab)) { fail(); break; }
-            }
+        if (lane == 0) {
+            s_issued[isb] = it;
+            // the commits' arrivals here have landed before the CTA exits (the copies: see the end of the kernel)
+            if (CG == 2 && !isb && !s_ab.flag)
+                for (uint32_t n = it > uint32_t(S) ? it - S : 0; n < it; n++)
+                    if (!g_wait(g_smem(&empty[n % S]), (n / S) & 1, &s_ab)) { fail(); break; }
         }
         __syncwarp();
     } else if (warp == 1 && rank == 0) {
@@ -255,6 +271,8 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
             const uint32_t idesc = I8 ? g_idesc_s8(T.bn, 128 * CG)
                                       : (g_idesc(T.bn, a.f16 != 0, 128 * CG) | (AMN ? G_IDESC_A_MN : 0u));
             const uint32_t d = tmem + (t & 1) * C::kAccCols;
+            const int half = T.bn / CG;
+            const uint32_t slice = (half <= 16 ? 16u : half <= 32 ? 32u : half <= 64 ? 64u : 128u) * 128u;
             if (t >= 2 && !g_wait_w(g_smem(&acc_empty[t & 1]), ((t >> 1) - 1) & 1, &s_ab)) {
                 ok = false;
                 break;
@@ -268,15 +286,18 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
                 }
                 g_fence_after();
                 const uint32_t sa = g_smem(ring + s * C::kStage), sb = sa + C::kMat * C::kABytes;
+                const int steps = min(4 * SL, (a.kdim - ks * C::kBK + C::kMmaK - 1) / C::kMmaK);
                 if (g_elect()) {
 #pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        const uint64_t bd = g_desc(sb + k * 32);
+                    for (int k = 0; k < 4 * SL; k++) {
+                        if (k >= steps) break;                     // K ends here
+                        const uint64_t bd = g_desc(sb + (k / 4) * slice + (k % 4) * 32);
                         const uint32_t acc = (k > 0 || ks > 0) ? 1u : 0u;
 #pragma unroll
                         for (int m = 0; m < C::kMat; m++) {
                             const uint32_t am = sa + m * C::kABytes;
-                            const uint64_t ad = AMN ? g_desc_mn(am + k * 2048, 8192) : g_desc(am + k * 32);
+                            const uint64_t ad = AMN ? g_desc_mn(am + k * 2048, SL * 8192)
+                                                    : g_desc(am + (k / 4) * 16384 + (k % 4) * 32);
                             if (I8) g_mma_s8<CG>(d + m * NT, ad, bd, idesc, acc);
                             else g_mma_f16<CG>(d + m * NT, ad, bd, idesc, acc);
                         }
@@ -361,16 +382,20 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
 
     g_fence_before();
     __syncthreads();
-    if (CG == 2) {
-        g_cluster_sync();
-        // after an expired wait, copies may be in flight whose stage only one CTA had issued: stand in for the
-        // other's arrival, then wait (bounded) for the last stages of both
-        if (rank == 0 && tid == 0) {
-            const uint32_t p0 = s_issued, p1 = g_ld_cluster(g_mapa(g_smem(&s_issued), 1));
-            const uint32_t lo = min(p0, p1), hi = max(p0, p1);
-            for (uint32_t n = lo; n < hi; n++) g_arrive(g_smem(&full[n % S]));
-            for (uint32_t n = hi > uint32_t(S) ? hi - S : 0; n < hi; n++) g_drain_wait(g_smem(&full[n % S]), (n / S) & 1);
+    if (CG == 2) g_cluster_sync();
+    // after an expired wait, copies may be in flight for a stage that only some producers had issued: stand in for
+    // the others' arrivals, then wait (bounded) for the last stages
+    if (rank == 0 && tid == 0) {
+        uint32_t n_[2 * CG], lo = 0xffffffffu, hi = 0;
+        for (int i = 0; i < 2 * CG; i++) {
+            n_[i] = i < 2 ? s_issued[i] : g_ld_cluster(g_mapa(g_smem(&s_issued[i & 1]), 1));
+            lo = min(lo, n_[i]);
+            hi = max(hi, n_[i]);
         }
+        for (uint32_t n = lo; n < hi; n++)
+            for (int i = 0; i < 2 * CG; i++)
+                if (n >= n_[i]) g_arrive(g_smem(&full[n % S]));
+        for (uint32_t n = hi > uint32_t(S) ? hi - S : 0; n < hi; n++) g_drain_wait(g_smem(&full[n % S]), (n / S) & 1);
     }
     g_fence_after();
     if (warp == 2) g_tmem_free<CG>(tmem, C::kTmem);
@@ -383,10 +408,10 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-template <bool I8, bool AMN, bool GU, int NT, int CG>
+template <bool I8, bool AMN, bool GU, int NT, int CG, int SL>
 static int mm_launch(const MmArgs& a, cudaStream_t s) {
-    using C = MmCfg<I8, AMN, GU, NT, CG>;
-    auto k = mm_kernel<I8, AMN, GU, NT, CG>;
+    using C = MmCfg<I8, AMN, GU, NT, CG, SL>;
+    auto k = mm_kernel<I8, AMN, GU, NT, CG, SL>;
     constexpr int kSmem = C::kStages * C::kStage + 1024 + 16 * kMaxE;
     int sms = 0;
     const int rc = mm_kernel_ready(reinterpret_cast<const void*>(k), kSmem, &sms);
@@ -394,6 +419,10 @@ static int mm_launch(const MmArgs& a, cudaStream_t s) {
     const int smem = C::kStages * C::kStage + 1024 + 16 * a.E;
     return mm_launch_cfg(k, dim3(sms / CG * CG), dim3(MM_THREADS), smem, CG, s, a);
 }
+
+// Tile shape by the average number of rows per expert: 0 (16 rows), 1 (64), 2 (256, a CTA pair; gate/up 128).
+static int mm_shape(const MmProblem& p) { return p.rows <= 16 * p.E ? 0 : p.rows <= 64 * p.E ? 1 : 2; }
+static int mm_slices(const MmProblem& p) { return mm_shape(p) == 0 || p.w1 ? 1 : 2; }
 
 static CUtensorMapDataType mm_type(bool i8, bool f16) {
     return i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : (f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
@@ -407,14 +436,26 @@ int launch_grouped_mm(const MmProblem& p, cudaStream_t s) {
     memset(&a, 0, sizeof(a));
     const int el = p.i8 ? 1 : 2, bk = 128 / el;
     const CUtensorMapDataType ty = mm_type(p.i8, p.f16);
-    // weights [E][out][in]: boxes of 128 features x 128 bytes of K, or (gradient) 64 features of `in` x 64 of K
+    // Tensor maps.  A row of 128-byte chunks, [chunks][rows][128 bytes], lets one copy bring both slices of a stage
+    // (gradient: both halves of A's features); it needs rows of whole chunks, else each slice is a copy.
+    const int sl = mm_slices(p);
     const uint64_t pitch = uint64_t(p.in_dim) * el, zp = pitch * p.out_dim;
-    const uint32_t bi = p.grad ? 64 : bk, br = p.grad ? 64 : 128;
-    int rc = g_map3(&a.a0, ty, p.w0, p.in_dim, p.out_dim, p.E, pitch, zp, bi, br);
-    if (rc == MOE_OK && p.w1) rc = g_map3(&a.a1, ty, p.w1, p.in_dim, p.out_dim, p.E, pitch, zp, bi, br);
     const int kdim = p.grad ? p.out_dim : p.in_dim;
-    if (rc == MOE_OK) rc = g_map(&a.b16, !p.i8, p.act, kdim, p.rows, uint64_t(kdim) * el, bk, 16, true);
-    if (rc == MOE_OK) rc = g_map(&a.b64, !p.i8, p.act, kdim, p.rows, uint64_t(kdim) * el, bk, 64, true);
+    const bool ca = p.in_dim % bk == 0 && (p.grad || sl == 2), cb = kdim % bk == 0 && sl == 2;
+    a.chunked = (ca ? 1 : 0) | (cb ? 2 : 0);
+    const uint32_t bi = p.grad ? 64 : bk, br = p.grad ? 64 * sl : 128;       // box: elements of a row, rows
+    int rc = MOE_OK;
+    for (int m = 0; m < 2 && rc == MOE_OK; m++) {
+        const void* w = m ? p.w1 : p.w0;
+        CUtensorMap* map = m ? &a.a1 : &a.a0;
+        if (!w) continue;
+        rc = ca ? g_map4(map, ty, w, bi, p.out_dim, p.in_dim / bk, p.E, pitch, zp, br)
+                : g_map3(map, ty, w, p.in_dim, p.out_dim, p.E, pitch, zp, bi, br);
+    }
+    for (int i = 0; i < MM_BOXES && rc == MOE_OK; i++)
+        rc = cb ? g_map4(&a.b[i], ty, p.act, bk, p.rows, kdim / bk, 1, uint64_t(kdim) * el, uint64_t(kdim) * el * p.rows,
+                         16u << i)
+                : g_map(&a.b[i], !p.i8, p.act, kdim, p.rows, uint64_t(kdim) * el, bk, 16u << i, true);
     if (rc != MOE_OK) return rc;
     a.offsets = p.offsets;
     a.row_slot = p.row_slot;
@@ -430,13 +471,17 @@ int launch_grouped_mm(const MmProblem& p, cudaStream_t s) {
     a.rows = p.rows;
     a.f16 = p.f16;
     a.early = p.i8;
-    const bool few = p.rows <= 16 * p.E;
-    if (p.i8) {
-        if (p.w1) return few ? mm_launch<true, false, true, 16, 1>(a, s) : mm_launch<true, false, true, 128, 1>(a, s);
-        return few ? mm_launch<true, false, false, 16, 1>(a, s) : mm_launch<true, false, false, 256, 1>(a, s);
+    switch (mm_shape(p)) {
+        case 0:
+            if (p.i8) return p.w1 ? mm_launch<true, false, true, 16, 1, 1>(a, s) : mm_launch<true, false, false, 16, 1, 1>(a, s);
+            return p.grad ? mm_launch<false, true, false, 16, 1, 1>(a, s) : mm_launch<false, false, false, 16, 1, 1>(a, s);
+        case 1:
+            if (p.i8) return p.w1 ? mm_launch<true, false, true, 64, 1, 1>(a, s) : mm_launch<true, false, false, 64, 1, 2>(a, s);
+            return p.grad ? mm_launch<false, true, false, 64, 1, 2>(a, s) : mm_launch<false, false, false, 64, 1, 2>(a, s);
+        default:
+            if (p.i8) return p.w1 ? mm_launch<true, false, true, 128, 2, 1>(a, s) : mm_launch<true, false, false, 256, 2, 2>(a, s);
+            return p.grad ? mm_launch<false, true, false, 256, 2, 2>(a, s) : mm_launch<false, false, false, 256, 2, 2>(a, s);
     }
-    if (p.grad) return few ? mm_launch<false, true, false, 16, 1>(a, s) : mm_launch<false, true, false, 256, 1>(a, s);
-    return few ? mm_launch<false, false, false, 16, 1>(a, s) : mm_launch<false, false, false, 256, 1>(a, s);
 }
 
 }  // namespace moe

@@ -11,9 +11,11 @@
 // memory, in both operands (a zero in one alone would still meet an infinity or a NaN in the other).
 //
 // A tile is (expert, 128 * CG output features, NT input features); a persistent CTA (or pair) takes every
-// grid-th tile.  Warp roles: 0 TMA producer, 1 MMA issuer (in a pair: the first CTA's), 2 zeroes the last block's
-// rows, 4-7 epilogue: tensor memory -> registers -> shared memory -> tile store (or fp32 reduction), which
-// clips at the tensor's edges.  Sums are fp32 in tensor memory; one rounding to the output type.
+// grid-th tile.  Warp roles: 0 and 3 TMA producers of dy and x, 1 MMA issuer (in a pair: the first CTA's), 2 zeroes the last block's
+// rows, 4-11 epilogue: tensor memory -> registers -> shared memory -> tile store (or fp32 reduction), which
+// clips at the tensor's edges.  The tensor core's fp32 sums are cut off rather than rounded, an error that grows with
+// the number of rows; so only 512 rows are summed in tensor memory at a time, and the epilogue adds those partial
+// sums in fp32 registers, rounded to nearest (a 65,536-row batch over 44 experts: 4.4e-6 of the result in one sum).
 #include <cstring>
 
 #include "grouped_mm.cuh"
@@ -21,15 +23,18 @@
 
 namespace moe {
 
-constexpr int WG_THREADS = 256;
+constexpr int WG_THREADS = 384;
+constexpr int WG_EPI_WARPS = 8;
 
 template <int NT, int CG>
 struct WgCfg {
     static constexpr int kBoxesB = NT / CG / 64;                  // 64-feature boxes of x this CTA stages
     static constexpr int kBox = 64 * 128;
     static constexpr int kStage = (2 + kBoxesB) * kBox;
-    static constexpr int kOutBytes = 4 * 2 * 4096;                // per epilogue warp: two 32-row x 128-byte buffers
-    static constexpr int kStages = (200 * 1024 - kOutBytes) / kStage;
+    static constexpr int kOutBytes = WG_EPI_WARPS * 2 * 4096;     // per epilogue warp: two 32-row x 128-byte buffers
+    static constexpr int kStages = (208 * 1024 - kOutBytes) / kStage;
+    static constexpr int kHalf = NT / 2;                          // columns of one epilogue warp
+    static constexpr int kChunk = 8;                              // K blocks summed in tensor memory at a time
     static constexpr int kTmem = 2 * NT;
     static_assert(kTmem <= 512 && kStages >= 3 && kStages <= 16, "tile shape");
 };
@@ -41,6 +46,7 @@ struct WgArgs {
     int32_t* status;
     int E, out_dim, in_dim, rows;
     int f16, out_f32, accumulate;
+    int chunked;                         // a and b are the views [1][features / 64][rows][64] (multiples of 64)
 };
 
 template <int NT, int CG>
@@ -49,7 +55,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
     constexpr int S = C::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ __align__(8) uint64_t full[S], empty[S], tail[S], acc_full[2], acc_empty[2], drain, hold_bar;
-    __shared__ uint32_t s_tmem, s_issued, s_tail;
+    __shared__ uint32_t s_tmem, s_issued[2], s_tail[2], s_tphase[2];      // of the producers of A and of B
     __shared__ int s_hold;
     __shared__ volatile GAbort s_ab;
 
@@ -59,20 +65,19 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
 
     if (tid == 0) {
         for (int s = 0; s < S; s++) {
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(g_smem(&full[s])), "r"(CG));
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(g_smem(&full[s])), "r"(2 * CG));
             asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(g_smem(&empty[s])));
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(g_smem(&tail[s])));
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 2;" ::"r"(g_smem(&tail[s])));
         }
         for (int s = 0; s < 2; s++) {
             asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(g_smem(&acc_full[s])));
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(g_smem(&acc_empty[s])), "r"(4 * CG));
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(g_smem(&acc_empty[s])), "r"(WG_EPI_WARPS * CG));
         }
         asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(g_smem(&drain)));
         asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(g_smem(&hold_bar)));
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         s_ab.flag = 0;
-        s_issued = 0;
-        s_tail = 0;
+        for (int i = 0; i < 2; i++) s_issued[i] = s_tail[i] = s_tphase[i] = 0;
     }
     if (warp == 2) g_tmem_alloc<CG>(g_smem(&s_tmem), C::kTmem);
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -95,13 +100,13 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
 
     const uint32_t tmem = s_tmem;
     const int per_e = MT * NTN;
-    const long long ntiles = (long long)a.E * per_e;
-    const long long tile0 = blockIdx.x / CG, tstep = gridDim.x / CG;
+    const int ntiles = a.E * per_e;
+    const int tile0 = int(blockIdx.x) / CG, tstep = int(gridDim.x) / CG;
     struct Tile { int e, base, n, m0, n0; };
-    auto tile_of = [&](long long tile) {
+    auto tile_of = [&](int tile) {
         Tile t;
-        t.e = int(tile / per_e);
-        const int local = int(tile - (long long)t.e * per_e);
+        t.e = tile / per_e;
+        const int local = tile - t.e * per_e;
         const int2 sp = span[t.e];
         t.base = sp.x;
         t.n = sp.y;
@@ -114,13 +119,19 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
         s_ab.flag = 1;
     };
 
-    if (warp == 0) {
-        // ---------------- producer (whole warp, one lane issues) ----------------
+    if (warp == 0 || warp == 3) {
+        // ---------------- producers of A (warp 0) and B (warp 3); one lane issues ----------------
+        constexpr int kMaxBoxes = C::kBoxesB > 2 ? C::kBoxesB : 2;
+        const bool isb = warp == 3;
+        const CUtensorMap* map = isb ? &a.b : &a.a;
+        const int boxes = isb ? C::kBoxesB : 2;
+        const uint32_t bytes = uint32_t(boxes) * C::kBox;
         uint32_t it = 0, tails = 0, tphase = 0;       // per stage: last fill was a tail; phase of its tail barrier
         bool ok = true;
-        for (long long tile = tile0; tile < ntiles && ok && !g_aborted(&s_ab); tile += tstep) {
+        for (int tile = tile0; tile < ntiles && ok && !g_aborted(&s_ab); tile += tstep) {
             const Tile T = tile_of(tile);
             const int KB = (T.n + 63) / 64;
+            const int x0 = isb ? T.n0 + int(rank) * (NT / CG) : T.m0 + int(rank) * 128;
             for (int kb = 0; kb < KB; kb++, it++) {
                 const int s = it % S;
                 if (it >= uint32_t(S) && !g_wait_w(g_smem(&empty[s]), ((it / S) - 1) & 1, &s_ab, 32)) {
@@ -139,16 +150,21 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
                     if (CG == 2) bar = g_mapa(bar, 0);
                     tails &= ~(1u << s);
                 }
+                const uint32_t d = g_smem(ring + s * C::kStage) + (isb ? 2 * C::kBox : 0);
+                const int r = T.base + kb * 64;
                 if (g_elect()) {
-                    if (CG == 2 && !tl) g_expect_remote(bar, C::kStage); else g_expect(bar, C::kStage);
-                    const uint32_t sa = g_smem(ring + s * C::kStage);
-                    const int r = T.base + kb * 64, m0 = T.m0 + int(rank) * 128, n0 = T.n0 + int(rank) * (NT / CG);
+                    if (CG == 2 && !tl) g_expect_remote(bar, bytes); else g_expect(bar, bytes);
 #pragma unroll
-                    for (int h = 0; h < 2 + C::kBoxesB; h++) {
-                        const CUtensorMap* map = h < 2 ? &a.a : &a.b;
-                        const int x = h < 2 ? m0 + h * 64 : n0 + (h - 2) * 64;
-                        if (CG == 2) g_tma2d_pair(sa + h * C::kBox, map, x, r, bar);
-                        else g_tma2d(sa + h * C::kBox, map, x, r, bar);
+                    for (int h = 0; h < kMaxBoxes; h++) {
+                        if (h >= boxes) break;
+                        if (a.chunked) {                           // two boxes of 64 features in one copy
+                            if (h & 1) continue;
+                            if (CG == 2) g_tma4d_pair(d + h * C::kBox, map, 0, r, x0 / 64 + h, 0, bar);
+                            else g_tma4d(d + h * C::kBox, map, 0, r, x0 / 64 + h, 0, bar);
+                        } else {
+                            if (CG == 2) g_tma2d_pair(d + h * C::kBox, map, x0 + h * 64, r, bar);
+                            else g_tma2d(d + h * C::kBox, map, x0 + h * 64, r, bar);
+                        }
                     }
                 }
                 __syncwarp();
@@ -156,21 +172,13 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
         }
         if (!ok) fail();
         if (lane == 0) {
-            const uint32_t first = it > uint32_t(S) ? it - S : 0;
-            if (s_ab.flag) {
-                // copies that complete here have landed before the CTA exits (a pair's other copies: below)
-                for (uint32_t n = first; n < it; n++) {
-                    const uint32_t s = n % S;
-                    if ((tails >> s) & 1) g_drain_wait(g_smem(&tail[s]), ((tphase >> s) & 1) ^ 1);
-                    else if (CG == 1) g_drain_wait(g_smem(&full[s]), (n / S) & 1);
-                }
-            } else if (CG == 2) {
-                // and so have the commits' arrivals
-                for (uint32_t n = first; n < it; n++)
+            s_issued[isb] = it;
+            s_tail[isb] = tails;
+            s_tphase[isb] = tphase;
+            // the commits' arrivals here have landed before the CTA exits (the copies: see the end of the kernel)
+            if (CG == 2 && !isb && !s_ab.flag)
+                for (uint32_t n = it > uint32_t(S) ? it - S : 0; n < it; n++)
                     if (!g_wait(g_smem(&empty[n % S]), (n / S) & 1, &s_ab)) { fail(); break; }
-            }
-            s_issued = it;
-            s_tail = tails;
         }
         __syncwarp();
     } else if (warp == 1 && rank == 0) {
@@ -180,17 +188,20 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
         uint32_t it = 0;
         int t = 0;
         bool ok = true;
-        for (long long tile = tile0; tile < ntiles && ok && !g_aborted(&s_ab); tile += tstep) {
+        for (int tile = tile0; tile < ntiles && ok && !g_aborted(&s_ab); tile += tstep) {
             const Tile T = tile_of(tile);
             if (T.n == 0) continue;
             const int KB = (T.n + 63) / 64;
-            const uint32_t d = tmem + (t & 1) * NT;
-            if (t >= 2 && !g_wait_w(g_smem(&acc_empty[t & 1]), ((t >> 1) - 1) & 1, &s_ab)) {
-                ok = false;
-                break;
-            }
-            g_fence_after();
-            for (int kb = 0; kb < KB; kb++, it++) {
+            for (int kb = 0; kb < KB && ok; kb++, it++) {
+                const int kc = kb % C::kChunk;
+                const uint32_t d = tmem + (t & 1) * NT;
+                if (kc == 0) {
+                    if (t >= 2 && !g_wait_w(g_smem(&acc_empty[t & 1]), ((t >> 1) - 1) & 1, &s_ab)) {
+                        ok = false;
+                        break;
+                    }
+                    g_fence_after();
+                }
                 const int s = it % S;
                 if (!g_wait_w(g_smem(&full[s]), (it / S) & 1, &s_ab)) {
                     ok = false;
@@ -199,16 +210,18 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
                 g_fence_after();
                 const uint32_t sa = g_smem(ring + s * C::kStage), sb = sa + 2 * C::kBox;
                 const int steps = min(4, (T.n - kb * 64 + 15) / 16);
+                const bool last = kc == C::kChunk - 1 || kb == KB - 1;
                 if (g_elect()) {
-                    for (int k = 0; k < steps; k++)
-                        g_mma_f16<CG>(d, g_desc_mn(sa + k * 2048, C::kBox), g_desc_mn(sb + k * 2048, C::kBox), idesc,
-                                      (k > 0 || kb > 0) ? 1u : 0u);
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        if (k < steps) g_mma_f16<CG>(d, g_desc_mn(sa + k * 2048, C::kBox), g_desc_mn(sb + k * 2048, C::kBox), idesc,
+                                      (k > 0 || kc > 0) ? 1u : 0u);
                     g_commit_cg<CG>(g_smem(&empty[s]));
-                    if (kb == KB - 1) g_commit_cg<CG>(g_smem(&acc_full[t & 1]));
+                    if (last) g_commit_cg<CG>(g_smem(&acc_full[t & 1]));
                 }
                 __syncwarp();
+                if (last) t++;
             }
-            t++;
         }
         if (!ok) fail();
         if (g_aborted(&s_ab)) {
@@ -221,7 +234,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
         // ---------------- zeros behind an expert's last row ----------------
         uint32_t it = 0, tphase = 0;
         bool ok = true;
-        for (long long tile = tile0; tile < ntiles && ok && !g_aborted(&s_ab); tile += tstep) {
+        for (int tile = tile0; tile < ntiles && ok && !g_aborted(&s_ab); tile += tstep) {
             const Tile T = tile_of(tile);
             const int KB = (T.n + 63) / 64;
             it += KB;
@@ -240,7 +253,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
             }
             g_fence_proxy_async();
             __syncwarp();
-            if (lane == 0) {
+            if (lane < 2) {                            // for both producers
                 if (CG == 2) g_arrive_remote(g_mapa(g_smem(&full[s]), 0)); else g_arrive(g_smem(&full[s]));
             }
             __syncwarp();
@@ -248,63 +261,50 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
         if (!ok) fail();
     } else if (warp >= 4) {
         // ---------------- epilogue ----------------
-        const int q = warp & 3;
+        const int q = warp & 3, c0 = (warp - 4) / 4 * C::kHalf;      // my lanes and columns
         const uint32_t lane_addr = uint32_t(q * 32) << 16;
-        uint8_t* buf = outb + q * 8192;
-        const int cols = a.out_f32 ? 32 : 64;                     // 128 bytes of a row
+        uint8_t* buf = outb + (warp - 4) * 8192;
         int t = 0, nst = 0;
         bool ok = true;
-        for (long long tile = tile0; tile < ntiles && !g_aborted(&s_ab); tile += tstep) {
+        for (int tile = tile0; tile < ntiles && ok && !g_aborted(&s_ab); tile += tstep) {
             const Tile T = tile_of(tile);
             if (T.n == 0 && a.accumulate) continue;
-            if (T.n > 0 && !g_wait_w(g_smem(&acc_full[t & 1]), (t >> 1) & 1, &s_ab, 32)) {
-                ok = false;
-                break;
+            const int m0 = T.m0 + int(rank) * 128 + q * 32, x0 = T.n0 + c0;
+            float sum[C::kHalf];
+#pragma unroll
+            for (int i = 0; i < C::kHalf; i++) sum[i] = 0.f;
+            const int chunks = ((T.n + 63) / 64 + C::kChunk - 1) / C::kChunk;
+            for (int ch = 0; ch < chunks; ch++, t++) {
+                if (!g_wait_w(g_smem(&acc_full[t & 1]), (t >> 1) & 1, &s_ab, 32)) {
+                    ok = false;
+                    break;
+                }
+                g_fence_after();
+                const uint32_t acc = tmem + lane_addr + (t & 1) * NT + c0;
+#pragma unroll
+                for (int c = 0; c < C::kHalf; c += 16) {
+                    uint32_t v[16];
+                    g_ld16(acc + c, v);
+                    g_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; i++) sum[c + i] += __uint_as_float(v[i]);
+                }
+                g_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    const uint32_t bar = g_smem(&acc_empty[t & 1]);
+                    if (CG == 2) g_arrive_remote(g_mapa(bar, 0)); else g_arrive(bar);
+                }
             }
-            g_fence_after();
-            const uint32_t acc = tmem + lane_addr + (t & 1) * NT;
-            const int m0 = T.m0 + int(rank) * 128 + q * 32;
-            for (int c = 0; c < NT; c += cols) {
-                const int x = T.n0 + c;
-                if (m0 >= a.out_dim || x >= a.in_dim) break;       // nothing of this tile past the tensor's edge
+            if (!ok) break;
+            // 128 bytes of 32 rows at a time; nothing of the tile is stored past the tensor's edge
+            auto put = [&](int x, auto piece) {
+                if (m0 >= a.out_dim || x >= a.in_dim) return;
                 uint8_t* st = buf + (nst & 1) * 4096;
                 if (lane == 0) g_store_wait_read<1>();              // the buffer's store before last has read it
                 __syncwarp();
-                uint4 o[8];
-                if (T.n == 0) {
 #pragma unroll
-                    for (int i = 0; i < 8; i++) o[i] = make_uint4(0, 0, 0, 0);
-                } else if (a.out_f32) {
-                    uint32_t v[2][16];
-                    g_ld16(acc + c, v[0]);
-                    g_ld16(acc + c + 16, v[1]);
-                    g_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 8; i++)
-                        o[i] = make_uint4(v[i / 4][4 * (i % 4)], v[i / 4][4 * (i % 4) + 1], v[i / 4][4 * (i % 4) + 2],
-                                          v[i / 4][4 * (i % 4) + 3]);
-                } else {
-                    uint32_t v[4][16];
-#pragma unroll
-                    for (int i = 0; i < 4; i++) g_ld16(acc + c + 16 * i, v[i]);
-                    g_ld_wait();
-                    uint32_t p[32];
-#pragma unroll
-                    for (int i = 0; i < 32; i++) {
-                        const float lo = __uint_as_float(v[i / 8][2 * (i % 8)]), hi = __uint_as_float(v[i / 8][2 * (i % 8) + 1]);
-                        if (a.f16) {
-                            const __half2 h = __floats2half2_rn(lo, hi);
-                            p[i] = *reinterpret_cast<const uint32_t*>(&h);
-                        } else {
-                            const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-                            p[i] = *reinterpret_cast<const uint32_t*>(&h);
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; i++) o[i] = make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
-                }
-#pragma unroll
-                for (int i = 0; i < 8; i++) *reinterpret_cast<uint4*>(st + g_swz(lane, i)) = o[i];
+                for (int i = 0; i < 8; i++) *reinterpret_cast<uint4*>(st + g_swz(lane, i)) = piece(i);
                 g_fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) {
@@ -312,15 +312,26 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
                     g_store_commit();
                 }
                 nst++;
-            }
-            if (T.n > 0) {
-                g_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    const uint32_t bar = g_smem(&acc_empty[t & 1]);
-                    if (CG == 2) g_arrive_remote(g_mapa(bar, 0)); else g_arrive(bar);
-                }
-                t++;
+            };
+            if (a.out_f32) {
+#pragma unroll
+                for (int c = 0; c < C::kHalf; c += 32)
+                    put(x0 + c, [&](int i) {
+                        return make_uint4(__float_as_uint(sum[c + 4 * i]), __float_as_uint(sum[c + 4 * i + 1]),
+                                          __float_as_uint(sum[c + 4 * i + 2]), __float_as_uint(sum[c + 4 * i + 3]));
+                    });
+            } else {
+                auto pair = [&](float lo, float hi) {
+                    const __half2 h = __floats2half2_rn(lo, hi);
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+                    return a.f16 ? *reinterpret_cast<const uint32_t*>(&h) : *reinterpret_cast<const uint32_t*>(&b);
+                };
+#pragma unroll
+                for (int c = 0; c < C::kHalf; c += 64)
+                    put(x0 + c, [&](int i) {
+                        const float* p = sum + c + 8 * i;
+                        return make_uint4(pair(p[0], p[1]), pair(p[2], p[3]), pair(p[4], p[5]), pair(p[6], p[7]));
+                    });
             }
         }
         if (!ok) fail();
@@ -330,21 +341,40 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
 
     g_fence_before();
     __syncthreads();
+    // After an expired wait copies may be in flight, for a stage that only some producers had issued: stand in for the
+    // others' arrivals, then wait (bounded) for the last stages.  First what completes on this CTA's tail barriers ...
+    if (tid == 0 && s_ab.flag) {
+        const int big = s_issued[1] > s_issued[0];
+        const uint32_t hi = s_issued[big], tl = s_tail[big], ph = s_tphase[big];
+        for (uint32_t n = hi > uint32_t(S) ? hi - S : 0; n < hi; n++) {
+            const uint32_t s = n % S;
+            if (!((tl >> s) & 1)) continue;
+            if (n >= s_issued[!big]) g_arrive(g_smem(&tail[s]));
+            g_drain_wait(g_smem(&tail[s]), ((ph >> s) & 1) ^ 1);
+        }
+    }
     if (CG == 2) {
+        __syncthreads();
         g_cluster_sync();
-        // after an expired wait: the pair's copies that complete on the first CTA's barriers (a stage that only
-        // one CTA had issued gets the other's arrival from here)
-        if (rank == 0 && tid == 0) {
-            const uint32_t p0 = s_issued, p1 = g_ld_cluster(g_mapa(g_smem(&s_issued), 1));
-            const uint32_t t1 = g_ld_cluster(g_mapa(g_smem(&s_tail), 1));
-            const uint32_t lo = min(p0, p1), hi = max(p0, p1), tl = p0 >= p1 ? s_tail : t1;
-            const bool aborted = s_ab.flag || g_ld_cluster(g_mapa(g_smem(const_cast<int*>(&s_ab.flag)), 1));
-            if (aborted) {
-                for (uint32_t n = hi > uint32_t(S) ? hi - S : 0; n < hi; n++) {
-                    if ((tl >> (n % S)) & 1) continue;
-                    if (n >= lo) g_arrive(g_smem(&full[n % S]));
-                    g_drain_wait(g_smem(&full[n % S]), (n / S) & 1);
+    }
+    // ... then what completes on the full barriers (a pair's: the first CTA's)
+    if (rank == 0 && tid == 0) {
+        bool aborted = s_ab.flag;
+        if (CG == 2) aborted |= g_ld_cluster(g_mapa(g_smem(const_cast<int*>(&s_ab.flag)), 1)) != 0;
+        if (aborted) {
+            uint32_t n_[2 * CG], hi = 0, tl = 0;
+            for (int i = 0; i < 2 * CG; i++) {
+                n_[i] = i < 2 ? s_issued[i] : g_ld_cluster(g_mapa(g_smem(&s_issued[i & 1]), 1));
+                if (n_[i] >= hi) {
+                    hi = n_[i];
+                    tl = i < 2 ? s_tail[i] : g_ld_cluster(g_mapa(g_smem(&s_tail[i & 1]), 1));
                 }
+            }
+            for (uint32_t n = hi > uint32_t(S) ? hi - S : 0; n < hi; n++) {
+                if ((tl >> (n % S)) & 1) continue;
+                for (int i = 0; i < 2 * CG; i++)
+                    if (n >= n_[i]) g_arrive(g_smem(&full[n % S]));
+                g_drain_wait(g_smem(&full[n % S]), (n / S) & 1);
             }
         }
     }
@@ -374,7 +404,12 @@ int launch_grouped_wgrad(const WgradProblem& p, cudaStream_t s) {
     memset(&a, 0, sizeof(a));
     const CUtensorMapDataType ty = p.f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     int rc = MOE_OK;
-    if (p.rows > 0) {
+    a.chunked = p.out_dim % 64 == 0 && p.in_dim % 64 == 0;
+    if (p.rows > 0 && a.chunked) {
+        rc = g_map4(&a.a, ty, p.dy, 64, p.rows, p.out_dim / 64, 1, uint64_t(p.out_dim) * 2, uint64_t(p.out_dim) * 2 * p.rows, 64);
+        if (rc == MOE_OK)
+            rc = g_map4(&a.b, ty, p.x, 64, p.rows, p.in_dim / 64, 1, uint64_t(p.in_dim) * 2, uint64_t(p.in_dim) * 2 * p.rows, 64);
+    } else if (p.rows > 0) {
         rc = g_map(&a.a, true, p.dy, p.out_dim, p.rows, uint64_t(p.out_dim) * 2, 64, 64, true);
         if (rc == MOE_OK) rc = g_map(&a.b, true, p.x, p.in_dim, p.rows, uint64_t(p.in_dim) * 2, 64, 64, true);
     }
@@ -383,6 +418,8 @@ int launch_grouped_wgrad(const WgradProblem& p, cudaStream_t s) {
         rc = g_map3(&a.d, p.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : ty, p.dw, p.in_dim, p.out_dim, p.E, pitch,
                     pitch * p.out_dim, p.out_f32 ? 32 : 64, 32);
     if (rc != MOE_OK) return rc;
+    // tile numbers are 32-bit
+    if (int64_t(p.E) * ((p.out_dim + 127) / 128) * ((p.in_dim + 127) / 128) > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
     a.offsets = p.offsets;
     a.status = p.status;
     a.E = p.E;
@@ -392,7 +429,7 @@ int launch_grouped_wgrad(const WgradProblem& p, cudaStream_t s) {
     a.f16 = p.f16;
     a.out_f32 = p.out_f32;
     a.accumulate = p.accumulate;
-    return wg_launch<128, 1>(a, s);
+    return a.out_dim > 128 ? wg_launch<256, 2>(a, s) : wg_launch<128, 1>(a, s);
 }
 
 }  // namespace moe

@@ -24,6 +24,18 @@ __device__ __forceinline__ void g_tma2d_pair(uint32_t dst, const CUtensorMap* ma
         "[%0], [%1, {%2, %3}], [%4];"
         ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar) : "memory");
 }
+__device__ __forceinline__ void g_tma4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void g_tma4d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                             uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar) : "memory");
+}
 __device__ __forceinline__ uint32_t g_cta_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -39,7 +51,7 @@ __device__ __forceinline__ void g_arrive_remote(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void g_expect_remote(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ uint32_t g_ld_cluster(uint32_t addr) {
     uint32_t v;
@@ -139,6 +151,21 @@ inline int g_map3(CUtensorMap* m, CUtensorMapDataType type, const void* base, ui
     cuuint32_t box[3] = {box_in, box_rows, 1};
     cuuint32_t es[3] = {1, 1, 1};
     const CUresult r = g_encode_fn_ref()(m, type, 3, const_cast<void*>(base), dims, strides, box, es,
+                                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
+}
+
+// Host: [z][rows][chunk * chunks] elements seen as [z][chunks][rows][chunk] (chunk: 128 bytes of a row): one box
+// holds box_rows rows of each of two neighbouring chunks.
+inline int g_map4(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint32_t chunk, uint64_t rows,
+                  uint64_t chunks, uint64_t z, uint64_t pitch, uint64_t zpitch, uint32_t box_rows) {
+    if ((reinterpret_cast<uintptr_t>(base) & 15u) || (pitch & 15u) || (zpitch & 15u)) return MOE_ERR_INVALID_ARG;
+    cuuint64_t dims[4] = {chunk, rows, chunks, z};
+    cuuint64_t strides[3] = {pitch, 128, zpitch};
+    cuuint32_t box[4] = {chunk, box_rows, 2, 1};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    const CUresult r = g_encode_fn_ref()(m, type, 4, const_cast<void*>(base), dims, strides, box, es,
                                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
