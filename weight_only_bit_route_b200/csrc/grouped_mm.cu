@@ -18,7 +18,7 @@
 //   warps 0, 3 TMA producers of A and B.  A stage is SL slices of K = 128 bytes (64 elements of 16 bits, 128 of 8)
 //              of A and B, 128-byte swizzled; rows past the tensors' ends arrive as zeros, and so does K past its end on both sides.
 //   warp 1     issues the MMAs (in a pair: the first CTA's warp, for both) and commits each stage.
-//   warps 4-7  epilogue from tensor memory: lane = feature, column = row.  Two accumulator buffers, so that the
+//   warps 4-11 epilogue from tensor memory: lane = feature, column = row.  Two accumulator buffers, so that the
 //              epilogue of a tile overlaps the next tile's products.
 // B's rows behind the tile's last are other experts' rows: their columns are computed and never stored.
 //
@@ -31,7 +31,8 @@
 
 namespace moe {
 
-constexpr int MM_THREADS = 256;
+constexpr int MM_THREADS = 384;
+constexpr int MM_EPI_WARPS = 8;
 constexpr int MM_BOXES = 4;
 
 // Tile shape of one instantiation.  NT: rows per tile; CG: CTAs per tile; SL: 128-byte slices of K per stage.
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
         }
         for (int s = 0; s < 2; s++) {
             asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(g_smem(&acc_full[s])));
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(g_smem(&acc_empty[s])), "r"(4 * CG));
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(g_smem(&acc_empty[s])), "r"(MM_EPI_WARPS * CG));
         }
         asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(g_smem(&drain)));
         asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(g_smem(&hold_bar)));
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
     uint8_t* ring = smem + ((1024u - (g_smem(smem) & 1023u)) & 1023u);
     int4* tbl = reinterpret_cast<int4*>(ring + S * C::kStage);      // active experts: {expert, first tile, first row, rows}
     {
-        constexpr int PER = kMaxE / MM_THREADS;
+        constexpr int PER = (kMaxE + MM_THREADS - 1) / MM_THREADS;
         int eb[PER], ne[PER], nt[PER], local = 0, ltiles = 0;
 #pragma unroll
         for (int i = 0; i < PER; i++) {
@@ -319,8 +320,11 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
     } else if (warp >= 4) {
         // ---------------- epilogue ----------------
         if (a.early) asm volatile("griddepcontrol.wait;" ::: "memory");      // the row pass's scales
-        const int q = warp & 3;
+        // Two warps per lane quarter, taking alternate blocks of 16 rows.  Lanes exchange halves of a pair of rows, so
+        // that each stores two features (4 bytes) of one row.
+        const int q = warp & 3, hsel = (warp - 4) >> 2, odd = lane & 1;
         const uint32_t lane_addr = uint32_t(q * 32) << 16;
+        constexpr int kScaleRegs = I8 ? (NT + 63) / 64 : 1;
         int t = 0;
         bool ok = true;
         for (int tile = tile0; tile < ntiles && !g_aborted(&s_ab); tile += tstep, t++) {
@@ -328,9 +332,26 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
             const int m = T.m0 + int(rank) * 128 + q * 32 + lane;            // my feature
             const bool mine = m < a.mdim;
             float w0 = 0.f, w1 = 0.f;
-            if (I8 && mine) {
-                w0 = a.s0[size_t(T.e) * a.mdim + m];
-                if (GU) w1 = a.s1[size_t(T.e) * a.mdim + m];
+            float rs[kScaleRegs];                                             // the scales of my blocks' rows
+            if (I8) {
+                if (mine) {
+                    w0 = a.s0[size_t(T.e) * a.mdim + m];
+                    if (GU) w1 = a.s1[size_t(T.e) * a.mdim + m];
+                }
+#pragma unroll
+                for (int i = 0; i < kScaleRegs; i++) {
+                    const int c = (4 * i + 2 * (lane >> 4) + hsel) * 16 + (lane & 15);   // lanes 0-15: block 2i, 16-31: 2i + 1
+                    rs[i] = 0.f;
+                    if (c < T.nval) {
+                        const int r = T.n0 + c;
+                        rs[i] = a.act_scale[r];
+                        if (!GU && a.topk_w) {
+                            const int slot = a.row_slot[r];
+                            if (slot >= 0 && slot < a.rows) rs[i] *= a.topk_w[slot];
+                            else { set_status(a.status, MOE_ERR_DEVICE_INDEX); rs[i] = 0.f; }
+                        }
+                    }
+                }
             }
             if (!g_wait_w(g_smem(&acc_full[t & 1]), (t >> 1) & 1, &s_ab, 32)) {
                 ok = false;
@@ -338,36 +359,41 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
             }
             g_fence_after();
             const uint32_t acc = tmem + lane_addr + (t & 1) * C::kAccCols;
-            uint16_t* dst = a.out + size_t(T.n0) * a.mdim + m;
-            for (int c = 0; c < T.nval; c += 16) {
+            uint16_t* dst = a.out + size_t(T.n0 + odd) * a.mdim + (m - odd);
+#pragma unroll
+            for (int i = 0; i < (NT + 31) / 32; i++) {
+                const int c = (2 * i + hsel) * 16;
+                if (c >= T.nval) break;
                 uint32_t v[16], u[16];
                 g_ld16(acc + c, v);
                 if constexpr (GU) g_ld16(acc + NT + c, u);
-                float rs = 0.f;                                               // lane j: the scale of row c + j
-                if (I8 && lane < 16 && c + lane < T.nval) {
-                    const int r = T.n0 + c + lane;
-                    rs = a.act_scale[r];
-                    if (!GU && a.topk_w) {
-                        const int slot = a.row_slot[r];
-                        if (slot >= 0 && slot < a.rows) rs *= a.topk_w[slot];
-                        else { set_status(a.status, MOE_ERR_DEVICE_INDEX); rs = 0.f; }
-                    }
-                }
                 g_ld_wait();
+                float y[16];
 #pragma unroll
                 for (int j = 0; j < 16; j++) {
-                    float y;
                     if constexpr (I8) {
                         // the 32-bit sum is rounded to fp32 once (2^-24), then scaled
-                        const float f = __shfl_sync(0xffffffffu, rs, j);
-                        y = float(int32_t(v[j])) * (f * w0);
-                        if constexpr (GU) y = y / (1.0f + expf(-y)) * (float(int32_t(u[j])) * (f * w1));
+                        const float f = __shfl_sync(0xffffffffu, rs[i / 2], (i & 1) * 16 + j);
+                        y[j] = float(int32_t(v[j])) * (f * w0);
+                        if constexpr (GU) y[j] = y[j] / (1.0f + expf(-y[j])) * (float(int32_t(u[j])) * (f * w1));
                     } else {
-                        y = __uint_as_float(v[j]);
+                        y[j] = __uint_as_float(v[j]);
                     }
-                    if (mine && c + j < T.nval)
-                        dst[size_t(c + j) * a.mdim] = (!I8 && a.f16) ? __half_as_ushort(__float2half_rn(y))
-                                                                      : __bfloat16_as_ushort(__float2bfloat16_rn(y));
+                }
+                uint16_t* row = dst + size_t(c) * a.mdim;
+#pragma unroll
+                for (int j = 0; j < 16; j += 2) {
+                    const float r = __shfl_xor_sync(0xffffffffu, odd ? y[j] : y[j + 1], 1);
+                    const float lo = odd ? r : y[j], hi = odd ? y[j + 1] : r;    // features m - odd, m - odd + 1
+                    uint32_t p;
+                    if (!I8 && a.f16) {
+                        const __half2 h = __floats2half2_rn(lo, hi);
+                        p = *reinterpret_cast<const uint32_t*>(&h);
+                    } else {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+                        p = *reinterpret_cast<const uint32_t*>(&h);
+                    }
+                    if (mine && c + j + odd < T.nval) *reinterpret_cast<uint32_t*>(row + size_t(j) * a.mdim) = p;
                 }
             }
             g_fence_before();
