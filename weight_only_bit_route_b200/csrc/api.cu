@@ -105,13 +105,28 @@ GemmBuffers gemm_buffers(void* base, int rows, int in_dim, bool act_ready, bool 
 bool i8_int4(const GemvProblem& p, int rows) {
     return p.fmt == MOE_FMT_INT4_G128 && p.E > 1 && rows <= kI8Int4MaxRows;
 }
-// A routed projection (or gate and up) in 8 bits: the rows are quantised into the pre-pass region (row scales, then
-// codes [rows, in]: part of what gemm_prep_bytes counts), then multiplied.
-int run_int8(const GemvProblem& p, bool gateup, int rows, int64_t nsrc, void* prep, cudaStream_t s) {
-    float* scales = reinterpret_cast<float*>(prep);
-    int8_t* codes = reinterpret_cast<int8_t*>(prep) + align256(size_t(rows) * 4);
-    MOE_TRY(launch_quant_int8(p.act, p.act_f16 != 0, rows, p.in_dim, p.act_by_token ? p.row_slot : nullptr, p.top_k,
-                              nsrc, p.offsets + p.E, codes, scales, p.status, s));
+// A routed projection (or gate and up) in 8 bits: the rows are quantised into the pre-pass region, then multiplied.
+// Gate/up takes its rows from the tokens.  A small batch quantises each row from its token; a large one quantises the
+// tokens once and copies their codes, less arithmetic for several rows a token.  The region holds the row scales, the
+// tokens' scales, the rows' codes and the tokens' codes: no more than gemm_prep_bytes counts for `rows` rows (there
+// are no more tokens than rows).
+constexpr int64_t kInt8TwoStep = int64_t(1) << 24;       // codes from which the copy pays for its launch
+int run_int8(const GemvProblem& p, bool gateup, int rows, int ntok, void* prep, cudaStream_t s) {
+    uint8_t* base = reinterpret_cast<uint8_t*>(prep);
+    float* scales = reinterpret_cast<float*>(base);
+    const bool two = gateup && rows >= 2 * ntok && int64_t(rows) * p.in_dim >= kInt8TwoStep;
+    int8_t* codes = reinterpret_cast<int8_t*>(base) + align256(size_t(rows) * 4) + (two ? align256(size_t(ntok) * 4) : 0);
+    if (two) {
+        float* tok_scales = reinterpret_cast<float*>(base + align256(size_t(rows) * 4));
+        int8_t* tok_codes = codes + align256(size_t(rows) * p.in_dim);
+        MOE_TRY(launch_quant_int8(p.act, p.act_f16 != 0, ntok, p.in_dim, nullptr, 1, ntok, nullptr, tok_codes, tok_scales,
+                                  p.status, s));
+        MOE_TRY(launch_gather_int8(tok_codes, tok_scales, rows, p.in_dim, p.row_slot, p.top_k, ntok, p.offsets + p.E, codes,
+                                   scales, p.status, s));
+    } else {
+        MOE_TRY(launch_quant_int8(p.act, p.act_f16 != 0, rows, p.in_dim, gateup ? p.row_slot : nullptr, p.top_k, ntok,
+                                  p.offsets + p.E, codes, scales, p.status, s));
+    }
     MmProblem m{};
     m.act = codes; m.act_scale = scales;
     m.w0 = p.p0; m.s0 = reinterpret_cast<const float*>(p.s0);
@@ -272,7 +287,7 @@ int layer_run(const void* x, int T, const moe_layer* L, void* y, void* ws, cudaS
     const bool i8 = routed_gemm && i8_int4(gu, R);
     if (int8) {
         MOE_TRY(run_int8(gu, true, R, T, prep, s));
-        MOE_TRY(run_int8(dn, false, R, R, prep, s));
+        MOE_TRY(run_int8(dn, false, R, T, prep, s));
     } else if (routed_gemm) {
         // 16-bit gate/up activation rows are gathered into the y_perm region,
         // free until the down projection writes it
@@ -495,7 +510,7 @@ int moe_grouped_w4a16_down(const void* h_perm, const int32_t* expert_offsets, co
     p.out = reinterpret_cast<__nv_bfloat16*>(y_perm); p.status = at<int32_t>(ws, 0);
     p.in_scale = down->input_scale;
     void* prep = at<void>(ws, kStepScratch + align256(size_t(E + 2) * 16));
-    if (down->fmt == MOE_FMT_INT8) return run_int8(p, false, rows, rows, prep, cs(stream));
+    if (down->fmt == MOE_FMT_INT8) return run_int8(p, false, rows, 0, prep, cs(stream));
     // BF16 rows are read in place (row r is activation row r)
     GemmBuffers b = gemm_buffers(prep, rows, F, down->fmt == MOE_FMT_BF16, i8_int4(p, rows));
     b.sched = p.status + 8;

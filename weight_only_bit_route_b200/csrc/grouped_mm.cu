@@ -47,10 +47,25 @@ struct MmCfg {
     static constexpr int kRingBytes = 200 * 1024;                 // beside it: the tile table (16 bytes per expert)
     static constexpr int kStages = kRingBytes / kStage < 12 ? kRingBytes / kStage : 12;
     static constexpr int kAccCols = kMat * NT;                    // one accumulator buffer
-    static constexpr int kTmem = 2 * kAccCols <= 32 ? 32 : (2 * kAccCols <= 64 ? 64 : (2 * kAccCols <= 128 ? 128 : (2 * kAccCols <= 256 ? 256 : 512)));
+    // Accumulators take tensor memory in two halves, in turn; a tile of more than kHalfRows rows takes both.
+    static constexpr int kHalfRows = 2 * kAccCols <= 512 ? NT : NT / 2;
+    static constexpr int kHalfCols = kMat * kHalfRows;
+    static constexpr int kTmemCols = 2 * kHalfCols;
+    static constexpr int kTmem = kTmemCols <= 32 ? 32 : (kTmemCols <= 64 ? 64 : (kTmemCols <= 128 ? 128 : (kTmemCols <= 256 ? 256 : 512)));
     static constexpr int kStep = 16 * CG;                         // a tile's N is a multiple of this
-    static_assert(2 * kAccCols <= 512 && NT % kStep == 0 && kStages >= 2, "tile shape");
+    static_assert(kAccCols <= 512 && NT % kStep == 0 && kStages >= 2, "tile shape");
     static_assert(NT / CG <= (16 << (MM_BOXES - 1)), "the largest box holds a tile's rows");
+};
+
+// The halves' use, kept alike by the issuer and the epilogue
+struct MmHalves {
+    uint32_t u0 = 0, u1 = 0, next = 0;                            // uses so far, the half whose turn it is
+    __device__ __forceinline__ uint32_t uses(uint32_t h) const { return h ? u1 : u0; }
+    __device__ __forceinline__ void take(uint32_t h, bool both) {
+        if (both || h == 0) u0++;
+        if (both || h == 1) u1++;
+        next = both ? 0 : h ^ 1u;
+    }
 };
 
 struct MmTile { int e, m0, n0, nval, bn; };                       // n0: first row (of all rows)
@@ -265,19 +280,23 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
         // failure testing (moe_set_wait_hold): wait for a barrier that nothing completes
         if (s_hold && !g_wait_w(g_smem(&hold_bar), 0, &s_ab)) fail();
         uint32_t it = 0;
-        int t = 0;
+        MmHalves acc;
         bool ok = true;
-        for (int tile = tile0; tile < ntiles && ok && !g_aborted(&s_ab); tile += tstep, t++) {
+        for (int tile = tile0; tile < ntiles && ok && !g_aborted(&s_ab); tile += tstep) {
             const MmTile T = tile_of(tile);
             const uint32_t idesc = I8 ? g_idesc_s8(T.bn, 128 * CG)
                                       : (g_idesc(T.bn, a.f16 != 0, 128 * CG) | (AMN ? G_IDESC_A_MN : 0u));
-            const uint32_t d = tmem + (t & 1) * C::kAccCols;
+            const bool both = T.bn > C::kHalfRows;
+            const uint32_t h = both ? 0 : acc.next;
+            const uint32_t d = tmem + h * C::kHalfCols, up = both ? NT : C::kHalfRows;
             const int half = T.bn / CG;
             const uint32_t slice = (half <= 16 ? 16u : half <= 32 ? 32u : half <= 64 ? 64u : 128u) * 128u;
-            if (t >= 2 && !g_wait_w(g_smem(&acc_empty[t & 1]), ((t >> 1) - 1) & 1, &s_ab)) {
+            if ((acc.uses(h) && !g_wait_w(g_smem(&acc_empty[h]), (acc.uses(h) - 1) & 1, &s_ab)) ||
+                (both && acc.u1 && !g_wait_w(g_smem(&acc_empty[1]), (acc.u1 - 1) & 1, &s_ab))) {
                 ok = false;
                 break;
             }
+            acc.take(h, both);
             g_fence_after();
             for (int ks = 0; ks < KS; ks++, it++) {
                 const int s = it % S;
@@ -293,18 +312,21 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
                     for (int k = 0; k < 4 * SL; k++) {
                         if (k >= steps) break;                     // K ends here
                         const uint64_t bd = g_desc(sb + (k / 4) * slice + (k % 4) * 32);
-                        const uint32_t acc = (k > 0 || ks > 0) ? 1u : 0u;
+                        const uint32_t add = (k > 0 || ks > 0) ? 1u : 0u;
 #pragma unroll
                         for (int m = 0; m < C::kMat; m++) {
                             const uint32_t am = sa + m * C::kABytes;
                             const uint64_t ad = AMN ? g_desc_mn(am + k * 2048, SL * 8192)
                                                     : g_desc(am + (k / 4) * 16384 + (k % 4) * 32);
-                            if (I8) g_mma_s8<CG>(d + m * NT, ad, bd, idesc, acc);
-                            else g_mma_f16<CG>(d + m * NT, ad, bd, idesc, acc);
+                            if (I8) g_mma_s8<CG>(d + m * up, ad, bd, idesc, add);
+                            else g_mma_f16<CG>(d + m * up, ad, bd, idesc, add);
                         }
                     }
                     g_commit_cg<CG>(g_smem(&empty[s]));
-                    if (ks == KS - 1) g_commit_cg<CG>(g_smem(&acc_full[t & 1]));
+                    if (ks == KS - 1) {
+                        g_commit_cg<CG>(g_smem(&acc_full[h]));
+                        if (both) g_commit_cg<CG>(g_smem(&acc_full[1]));
+                    }
                 }
                 __syncwarp();
             }
@@ -325,9 +347,9 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
         const int q = warp & 3, hsel = (warp - 4) >> 2, odd = lane & 1;
         const uint32_t lane_addr = uint32_t(q * 32) << 16;
         constexpr int kScaleRegs = I8 ? (NT + 63) / 64 : 1;
-        int t = 0;
+        MmHalves use;
         bool ok = true;
-        for (int tile = tile0; tile < ntiles && !g_aborted(&s_ab); tile += tstep, t++) {
+        for (int tile = tile0; tile < ntiles && !g_aborted(&s_ab); tile += tstep) {
             const MmTile T = tile_of(tile);
             const int m = T.m0 + int(rank) * 128 + q * 32 + lane;            // my feature
             const bool mine = m < a.mdim;
@@ -353,12 +375,15 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
                     }
                 }
             }
-            if (!g_wait_w(g_smem(&acc_full[t & 1]), (t >> 1) & 1, &s_ab, 32)) {
+            const bool both = T.bn > C::kHalfRows;
+            const uint32_t h = both ? 0 : use.next;
+            if (!g_wait_w(g_smem(&acc_full[h]), use.uses(h) & 1, &s_ab, 32) ||
+                (both && !g_wait_w(g_smem(&acc_full[1]), use.u1 & 1, &s_ab, 32))) {
                 ok = false;
                 break;
             }
             g_fence_after();
-            const uint32_t acc = tmem + lane_addr + (t & 1) * C::kAccCols;
+            const uint32_t acc = tmem + lane_addr + h * C::kHalfCols, up = both ? NT : C::kHalfRows;
             uint16_t* dst = a.out + size_t(T.n0 + odd) * a.mdim + (m - odd);
 #pragma unroll
             for (int i = 0; i < (NT + 31) / 32; i++) {
@@ -366,7 +391,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
                 if (c >= T.nval) break;
                 uint32_t v[16], u[16];
                 g_ld16(acc + c, v);
-                if constexpr (GU) g_ld16(acc + NT + c, u);
+                if constexpr (GU) g_ld16(acc + up + c, u);
                 g_ld_wait();
                 float y[16];
 #pragma unroll
@@ -375,7 +400,9 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
                         // the 32-bit sum is rounded to fp32 once (2^-24), then scaled
                         const float f = __shfl_sync(0xffffffffu, rs[i / 2], (i & 1) * 16 + j);
                         y[j] = float(int32_t(v[j])) * (f * w0);
-                        if constexpr (GU) y[j] = y[j] / (1.0f + expf(-y[j])) * (float(int32_t(u[j])) * (f * w1));
+                        // (silu with the approximate exponential and division: a relative error below
+                        // (1 + |g|) 2^-21, beside the 2^-9 of the bf16 result; an exponential that overflows gives 0)
+                        if constexpr (GU) y[j] = __fdividef(y[j], 1.0f + __expf(-y[j])) * (float(int32_t(u[j])) * (f * w1));
                     } else {
                         y[j] = __uint_as_float(v[j]);
                     }
@@ -399,9 +426,12 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
             g_fence_before();
             __syncwarp();
             if (lane == 0) {
-                const uint32_t bar = g_smem(&acc_empty[t & 1]);
-                if (CG == 2) g_arrive_remote(g_mapa(bar, 0)); else g_arrive(bar);
+                for (uint32_t i = h; i <= (both ? 1u : h); i++) {
+                    const uint32_t bar = g_smem(&acc_empty[i]);
+                    if (CG == 2) g_arrive_remote(g_mapa(bar, 0)); else g_arrive(bar);
+                }
             }
+            use.take(h, both);
         }
         if (!ok) fail();
     }
@@ -412,13 +442,12 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
     // after an expired wait, copies may be in flight for a stage that only some producers had issued: stand in for
     // the others' arrivals, then wait (bounded) for the last stages
     if (rank == 0 && tid == 0) {
-        uint32_t n_[2 * CG], lo = 0xffffffffu, hi = 0;
+        uint32_t n_[2 * CG], hi = 0;
         for (int i = 0; i < 2 * CG; i++) {
             n_[i] = i < 2 ? s_issued[i] : g_ld_cluster(g_mapa(g_smem(&s_issued[i & 1]), 1));
-            lo = min(lo, n_[i]);
             hi = max(hi, n_[i]);
         }
-        for (uint32_t n = lo; n < hi; n++)
+        for (uint32_t n = hi > uint32_t(S) ? hi - S : 0; n < hi; n++)
             for (int i = 0; i < 2 * CG; i++)
                 if (n >= n_[i]) g_arrive(g_smem(&full[n % S]));
         for (uint32_t n = hi > uint32_t(S) ? hi - S : 0; n < hi; n++) g_drain_wait(g_smem(&full[n % S]), (n / S) & 1);
@@ -446,7 +475,7 @@ static int mm_launch(const MmArgs& a, cudaStream_t s) {
     return mm_launch_cfg(k, dim3(sms / CG * CG), dim3(MM_THREADS), smem, CG, s, a);
 }
 
-// Tile shape by the average number of rows per expert: 0 (16 rows), 1 (64), 2 (256, a CTA pair; gate/up 128).
+// Tile shape by the average number of rows per expert: 0 (16 rows), 1 (64), 2 (256, a CTA pair).
 static int mm_shape(const MmProblem& p) { return p.rows <= 16 * p.E ? 0 : p.rows <= 64 * p.E ? 1 : 2; }
 static int mm_slices(const MmProblem& p) { return mm_shape(p) == 0 || p.w1 ? 1 : 2; }
 
@@ -505,7 +534,7 @@ int launch_grouped_mm(const MmProblem& p, cudaStream_t s) {
             if (p.i8) return p.w1 ? mm_launch<true, false, true, 64, 1, 1>(a, s) : mm_launch<true, false, false, 64, 1, 2>(a, s);
             return p.grad ? mm_launch<false, true, false, 64, 1, 2>(a, s) : mm_launch<false, false, false, 64, 1, 2>(a, s);
         default:
-            if (p.i8) return p.w1 ? mm_launch<true, false, true, 128, 2, 1>(a, s) : mm_launch<true, false, false, 256, 2, 2>(a, s);
+            if (p.i8) return p.w1 ? mm_launch<true, false, true, 256, 2, 1>(a, s) : mm_launch<true, false, false, 256, 2, 2>(a, s);
             return p.grad ? mm_launch<false, true, false, 256, 2, 2>(a, s) : mm_launch<false, false, false, 256, 2, 2>(a, s);
     }
 }

@@ -46,6 +46,9 @@ int launch_grouped_wgrad(const WgradProblem& p, cudaStream_t s);
 int launch_quant_int8(const void* x, bool f16, int64_t rows, int64_t cols, const int32_t* row_slot, int top_k,
                       int64_t nsrc, const int32_t* nrows, int8_t* codes, float* scales, int32_t* status,
                       cudaStream_t s);
+// Rows of codes and their scales by slot, as above, from the nsrc rows src, src_scales.
+int launch_gather_int8(const int8_t* src, const float* src_scales, int rows, int cols, const int32_t* row_slot, int top_k,
+                       int nsrc, const int32_t* nrows, int8_t* codes, float* scales, int32_t* status, cudaStream_t s);
 
 // One-time set-up of a kernel on the current device: its shared-memory attribute; *sms: the device's SM count.
 int mm_kernel_ready(const void* kernel, int smem_bytes, int* sms);

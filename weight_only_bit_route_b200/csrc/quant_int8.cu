@@ -6,7 +6,7 @@
 // The codes are those of the real quotient: 127 x has at most 18 significant bits, so a quotient that is no tie
 // lies at least 2^-21 of its size away from one, further than fp32 rounds; the division in fp32 (IEEE) then
 // rounds to the same side, and a tie is exact.  The kernel multiplies by 127 / max|x| first (within 2^-16 of
-// the quotient) and divides only where that lands within 2^-12 of a tie.
+// the quotient) and divides only where one of eight neighbours lands within 2^-12 of a tie.
 //
 // One block per row, the row's first 4096 elements kept in registers between the two passes.  Bound by the
 // row's bytes: 2 read and 1 written per element.
@@ -25,15 +25,20 @@ __device__ __forceinline__ uint32_t q8_max8(uint32_t m, const uint4& v) {
     return q8_max2(q8_max2(q8_max2(q8_max2(m, v.x), v.y), v.z), v.w);
 }
 
-__device__ __forceinline__ int q8_code(float x, float r, float amax, bool slow) {
-    const float t = x * r;
-    float k = rintf(t);
-    if (slow || fabsf(t - k) > 0.5f - 0x1p-12f) {
-        // near a tie, or a row so small that 127 / amax overflows.  Powers of two keep 127 x in range.
-        const float c = amax > 0x1p100f ? 0x1p-16f : (amax < 0x1p-90f ? 0x1p64f : 1.f);
-        k = rintf(__fdiv_rn(127.f * (x * c), amax * c));
-    }
-    return int(k);
+// rint(t) for |t| < 2^22 as a float sum: t + 1.5 2^23 has the whole number in its low bits (ties to even), without
+// the conversion instructions, which run at a quarter of the rate
+constexpr float Q8_MAGIC = 12582912.f;
+
+// The code by division: near a tie, or in a row so small that 127 / amax overflows.  Powers of two keep 127 x in range.
+__device__ __forceinline__ uint32_t q8_divide(float x, float amax) {
+    const float c = amax > 0x1p100f ? 0x1p-16f : (amax < 0x1p-90f ? 0x1p64f : 1.f);
+    return __float_as_uint(rintf(__fdiv_rn(127.f * (x * c), amax * c)) + Q8_MAGIC);
+}
+
+// The token of a slot, or -1
+__device__ __forceinline__ long long q8_source(int slot, int top_k, long long nsrc) {
+    const int t = slot / top_k;
+    return slot >= 0 && t < nsrc ? t : -1;
 }
 
 template <bool F16>
@@ -46,20 +51,14 @@ __global__ void __launch_bounds__(Q8_THREADS) quant_int8_kernel(const uint16_t* 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the product's weights need nothing from here
     const long long row = blockIdx.x;
     if (nrows && row >= *nrows) return;                               // behind the last expert's rows
-    long long src = row;
-    if (row_slot) {
-        src = row_slot[row] / top_k;
-        if (row_slot[row] < 0 || src >= nsrc) {
-            if (threadIdx.x == 0) {
-                if (status) set_status(status, MOE_ERR_DEVICE_INDEX);
-                scales[row] = 0.f;
-            }
-            src = -1;
-        }
-    }
     const long long n = cols / 8;
     uint2* dst = reinterpret_cast<uint2*>(codes + row * cols);
-    if (src < 0) {
+    const long long src = row_slot ? q8_source(row_slot[row], top_k, nsrc) : row;
+    if (src < 0) {                                                    // a slot out of range: a zero row
+        if (threadIdx.x == 0) {
+            scales[row] = 0.f;
+            if (status) set_status(status, MOE_ERR_DEVICE_INDEX);
+        }
         for (long long i = threadIdx.x; i < n; i += Q8_THREADS) dst[i] = make_uint2(0, 0);
         return;
     }
@@ -88,18 +87,26 @@ __global__ void __launch_bounds__(Q8_THREADS) quant_int8_kernel(const uint16_t* 
     }
     const bool zero = bad || m == 0;
     const float r = __fdiv_rn(127.f, amax);
-    const bool slow = amax < 0x1p-90f;
+    const bool slow = amax < 0x1p-90f && !zero;
     auto put = [&](long long i, const uint4& v) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t o[2] = {0, 0};
-        if (!zero) {
+        uint32_t c[8];
+        float far = 0.f;                                              // largest distance from the whole number
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const int lo = q8_code(act_lo<F16>(w[j]), r, amax, slow), hi = q8_code(act_hi<F16>(w[j]), r, amax, slow);
-                o[j >> 1] |= ((uint32_t(lo) & 0xffu) | ((uint32_t(hi) & 0xffu) << 8)) << (16 * (j & 1));
-            }
+        for (int j = 0; j < 8; j++) {
+            const float t = ((j & 1) ? act_hi<F16>(w[j >> 1]) : act_lo<F16>(w[j >> 1])) * r;
+            const float k = t + Q8_MAGIC;
+            far = fmaxf(far, fabsf(t - (k - Q8_MAGIC)));
+            c[j] = __float_as_uint(k);
         }
-        dst[i] = make_uint2(o[0], o[1]);
+        if (slow || far > 0.5f - 0x1p-12f)
+#pragma unroll
+            for (int j = 0; j < 8; j++) c[j] = q8_divide((j & 1) ? act_hi<F16>(w[j >> 1]) : act_lo<F16>(w[j >> 1]), amax);
+        uint2 o = make_uint2(0, 0);
+        if (!zero)
+            o = make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410),
+                           __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410));
+        dst[i] = o;
     };
 #pragma unroll
     for (int j = 0; j < Q8_KEEP; j++) {
@@ -116,6 +123,33 @@ int launch_quant_int8(const void* x, bool f16, int64_t rows, int64_t cols, const
     auto k = f16 ? quant_int8_kernel<true> : quant_int8_kernel<false>;
     return mm_launch_cfg(k, dim3(unsigned(rows)), dim3(Q8_THREADS), 0, 1, s, static_cast<const uint16_t*>(x),
                          (long long)cols, row_slot, top_k, (long long)nsrc, nrows, codes, scales, status);
+}
+
+// One block per row, 16 bytes per thread and step.
+__global__ void __launch_bounds__(Q8_THREADS) gather_int8_kernel(const int8_t* __restrict__ src,
+                                                                 const float* __restrict__ src_scales, int cols,
+                                                                 const int32_t* __restrict__ row_slot, int top_k, int nsrc,
+                                                                 const int32_t* __restrict__ nrows,
+                                                                 int8_t* __restrict__ codes, float* __restrict__ scales,
+                                                                 int32_t* status) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int row = blockIdx.x;
+    if (row >= *nrows) return;
+    const long long t = q8_source(row_slot[row], top_k, nsrc);
+    if (threadIdx.x == 0) {
+        scales[row] = t < 0 ? 0.f : src_scales[t];
+        if (t < 0) set_status(status, MOE_ERR_DEVICE_INDEX);
+    }
+    const uint4* p = reinterpret_cast<const uint4*>(src + (t < 0 ? 0 : t) * cols);
+    uint4* d = reinterpret_cast<uint4*>(codes + size_t(row) * cols);
+    for (int i = threadIdx.x; i < cols / 16; i += Q8_THREADS) __stcs(d + i, t < 0 ? make_uint4(0, 0, 0, 0) : p[i]);
+}
+
+int launch_gather_int8(const int8_t* src, const float* src_scales, int rows, int cols, const int32_t* row_slot, int top_k,
+                       int nsrc, const int32_t* nrows, int8_t* codes, float* scales, int32_t* status, cudaStream_t s) {
+    return mm_launch_cfg(gather_int8_kernel, dim3(unsigned(rows)), dim3(Q8_THREADS), 0, 1, s, src, src_scales, cols,
+                         row_slot, top_k, nsrc, nrows, codes, scales, status);
 }
 
 // Per device and kernel: the shared-memory attribute, set once under a lock.
