@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
             if (lane == 0) {
                 for (uint32_t i = h; i <= (both ? 1u : h); i++) {
                     const uint32_t bar = g_smem(&acc_empty[i]);
-                    if (CG == 2) g_arrive_remote(g_mapa(bar, 0)); else g_arrive(bar);
+                    if (CG == 2) g_arrive_remote_relaxed(g_mapa(bar, 0)); else g_arrive(bar);
                 }
             }
             use.take(h, both);
@@ -507,7 +507,8 @@ int launch_grouped_mm(const MmProblem& p, cudaStream_t s) {
         rc = ca ? g_map4(map, ty, w, bi, p.out_dim, p.in_dim / bk, p.E, pitch, zp, br)
                 : g_map3(map, ty, w, p.in_dim, p.out_dim, p.E, pitch, zp, bi, br);
     }
-    for (int i = 0; i < MM_BOXES && rc == MOE_OK; i++)
+    const int boxes = mm_shape(p) == 0 ? 1 : mm_shape(p) == 1 ? 3 : MM_BOXES;     // those a tile of this shape can ask for
+    for (int i = 0; i < boxes && rc == MOE_OK; i++)
         rc = cb ? g_map4(&a.b[i], ty, p.act, bk, p.rows, kdim / bk, 1, uint64_t(kdim) * el, uint64_t(kdim) * el * p.rows,
                          16u << i)
                 : g_map(&a.b[i], !p.i8, p.act, kdim, p.rows, uint64_t(kdim) * el, bk, 16u << i, true);

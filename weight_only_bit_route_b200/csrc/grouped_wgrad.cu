@@ -36,6 +36,7 @@ struct WgCfg {
     static constexpr int kHalf = NT / 2;                          // columns of one epilogue warp
     static constexpr int kChunk = 8;                              // K blocks summed in tensor memory at a time
     static constexpr int kTmem = 2 * NT;
+    static_assert(kBoxesB % 2 == 0, "one copy brings two boxes");
     static_assert(kTmem <= 512 && kStages >= 3 && kStages <= 16, "tile shape");
 };
 
@@ -293,7 +294,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
                 __syncwarp();
                 if (lane == 0) {
                     const uint32_t bar = g_smem(&acc_empty[t & 1]);
-                    if (CG == 2) g_arrive_remote(g_mapa(bar, 0)); else g_arrive(bar);
+                    if (CG == 2) g_arrive_remote_relaxed(g_mapa(bar, 0)); else g_arrive(bar);
                 }
             }
             if (!ok) break;

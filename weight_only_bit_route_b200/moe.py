@@ -104,8 +104,13 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# the current stream of a device as an integer (torch.cuda.current_stream builds a Stream object: 3 us a call)
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    return _raw_stream(torch.cuda.current_device())
 
 
 class Bank:
@@ -228,7 +233,7 @@ def permute_noalloc(ids, E):
 
 def grouped_swiglu(x, offsets, row_slot, top_k, gate, up, rows, ws, out=None):
     T, H = x.shape
-    h = out if out is not None else torch.empty(rows, gate.out_dim, dtype=torch.bfloat16, device=x.device)
+    h = out if out is not None else x.new_empty((rows, gate.out_dim), dtype=torch.bfloat16)
     g, u = gate.struct(), up.struct()
     _check("moe_grouped_w4a16_swiglu",
            lib.moe_grouped_w4a16_swiglu(_ptr(x), T, H, _ptr(offsets), _ptr(row_slot), top_k,
@@ -239,7 +244,7 @@ def grouped_swiglu(x, offsets, row_slot, top_k, gate, up, rows, ws, out=None):
 
 def grouped_down(h_perm, offsets, row_slot, topk_w, down, ws, out=None):
     rows = h_perm.shape[0]
-    y = out if out is not None else torch.empty(rows, down.out_dim, dtype=torch.bfloat16, device=h_perm.device)
+    y = out if out is not None else h_perm.new_empty((rows, down.out_dim), dtype=torch.bfloat16)
     d = down.struct()
     _check("moe_grouped_w4a16_down",
            lib.moe_grouped_w4a16_down(_ptr(h_perm), _ptr(offsets), _ptr(row_slot), _ptr(topk_w), rows,
@@ -247,59 +252,59 @@ def grouped_down(h_perm, offsets, row_slot, topk_w, down, ws, out=None):
     return y
 
 
-def _need(fn, ok, what):
-    if not ok:
-        raise MoEError(f"{fn}: {what}", -1)
-
-
-def _mm_args(fn, offsets, ws, **tensors):
-    """Checks what the C entry cannot see: types, shapes' agreement, contiguity, one device."""
-    ts = list(tensors.values())
-    dt, dev = ts[0].dtype, ts[0].device
-    _need(fn, dt in (torch.bfloat16, torch.float16), "bf16 or fp16 tensors")
-    for name, t in tensors.items():
-        _need(fn, t.dtype == dt, f"{name} has another type")
-    for name, t in dict(tensors, offsets=offsets, ws=ws).items():
-        _need(fn, t.device == dev and t.is_cuda, f"{name} is not on the tensors' CUDA device")
-        _need(fn, t.is_contiguous(), f"{name} is not contiguous")
-    _need(fn, offsets.dtype == torch.int32 and offsets.dim() == 1 and offsets.numel() >= 2, "offsets: int32 [E+1]")
-    return offsets.numel() - 1, int(dt == torch.float16)
+def _mm_check(fn, a, b, offsets, ws, shapes_ok, shapes):
+    """Checks what the C entry cannot see: types, agreement of the shapes, contiguity, one device."""
+    dt, dev = a.dtype, a.get_device()
+    if not (b.dtype is dt and (dt is torch.bfloat16 or dt is torch.float16) and dev >= 0 and b.get_device() == dev
+            and offsets.get_device() == dev and ws.get_device() == dev and a.is_contiguous() and b.is_contiguous()
+            and offsets.is_contiguous() and ws.is_contiguous() and offsets.dtype is torch.int32 and offsets.dim() == 1
+            and offsets.numel() >= 2 and ws.dtype is torch.uint8 and shapes_ok):
+        raise MoEError(f"{fn}: needs {shapes} of one type (bf16 or fp16), offsets int32 [E+1] and a uint8 workspace, "
+                       "all contiguous and on one CUDA device", -1)
+    return dev
 
 
 def _mm_out(fn, out, shape, dtype, like):
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    _need(fn, tuple(out.shape) == tuple(shape) and out.dtype == dtype and out.device == like.device
-          and out.is_contiguous(), f"out must be contiguous {dtype} {tuple(shape)} on the tensors' device")
+        return like.new_empty(shape, dtype=dtype)
+    if not (tuple(out.shape) == shape and out.dtype is dtype and out.device == like.device and out.is_contiguous()):
+        raise MoEError(f"{fn}: out must be contiguous {dtype} {shape} on the tensors' device", -1)
     return out
+
+
+def _on(dev, fn, call, *args):
+    """The call with the tensors' device current, on its current stream."""
+    if torch.cuda.current_device() == dev:
+        code = call(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            code = call(*args, _raw_stream(dev))
+    if code != 0:
+        raise MoEError(fn, code)
 
 
 def grouped_mm(x, w, offsets, ws, out=None):
     """y[r] = w[e] x[r] for the rows r of each expert e (bf16 or fp16): x [rows, in], w [E, out, in] -> [rows, out].
     Rows outside every expert are not written."""
     fn = "moe_grouped_mm"
-    E, f16 = _mm_args(fn, offsets, ws, x=x, w=w)
-    _need(fn, x.dim() == 2 and w.dim() == 3 and w.shape[0] == E and w.shape[2] == x.shape[1],
-          "x [rows, in], w [E, out, in]")
-    rows, (_, n_out, n_in) = x.shape[0], w.shape
-    y = _mm_out(fn, out, (rows, n_out), x.dtype, x)
-    with torch.cuda.device(x.device):
-        _check(fn, lib.moe_grouped_mm(_ptr(x), _ptr(offsets), rows, _ptr(w), E, n_out, n_in, f16, _ptr(y), _ptr(ws),
-                                      ws.numel(), _stream()))
+    sx, sw = x.shape, w.shape
+    dev = _mm_check(fn, x, w, offsets, ws, len(sx) == 2 and len(sw) == 3 and sw[0] == offsets.numel() - 1
+                    and sw[2] == sx[1], "x [rows, in], w [E, out, in]")
+    y = _mm_out(fn, out, (sx[0], sw[1]), x.dtype, x)
+    _on(dev, fn, lib.moe_grouped_mm, x.data_ptr(), offsets.data_ptr(), sx[0], w.data_ptr(), sw[0], sw[1], sw[2],
+        x.dtype is torch.float16, y.data_ptr(), ws.data_ptr(), ws.numel())
     return y
 
 
 def grouped_mm_dgrad(dy, w, offsets, ws, out=None):
     """Gradient of grouped_mm by x: dx[r] = w[e]^T dy[r]; dy [rows, out], w [E, out, in] -> [rows, in]."""
     fn = "moe_grouped_mm_dgrad"
-    E, f16 = _mm_args(fn, offsets, ws, dy=dy, w=w)
-    _need(fn, dy.dim() == 2 and w.dim() == 3 and w.shape[0] == E and w.shape[1] == dy.shape[1],
-          "dy [rows, out], w [E, out, in]")
-    rows, (_, n_out, n_in) = dy.shape[0], w.shape
-    dx = _mm_out(fn, out, (rows, n_in), dy.dtype, dy)
-    with torch.cuda.device(dy.device):
-        _check(fn, lib.moe_grouped_mm_dgrad(_ptr(dy), _ptr(offsets), rows, _ptr(w), E, n_out, n_in, f16, _ptr(dx),
-                                            _ptr(ws), ws.numel(), _stream()))
+    sy, sw = dy.shape, w.shape
+    dev = _mm_check(fn, dy, w, offsets, ws, len(sy) == 2 and len(sw) == 3 and sw[0] == offsets.numel() - 1
+                    and sw[1] == sy[1], "dy [rows, out], w [E, out, in]")
+    dx = _mm_out(fn, out, (sy[0], sw[2]), dy.dtype, dy)
+    _on(dev, fn, lib.moe_grouped_mm_dgrad, dy.data_ptr(), offsets.data_ptr(), sy[0], w.data_ptr(), sw[0], sw[1], sw[2],
+        dy.dtype is torch.float16, dx.data_ptr(), ws.data_ptr(), ws.numel())
     return dx
 
 
@@ -307,17 +312,18 @@ def grouped_mm_wgrad(dy, x, offsets, ws, out=None, out_dtype=None, accumulate=Fa
     """Gradient of grouped_mm by w: dw[e] = sum over e's rows of dy[r] x[r]^T -> [E, out, in], in the tensors'
     type or fp32.  accumulate: add to `out` (fp32) instead."""
     fn = "moe_grouped_mm_wgrad"
-    E, f16 = _mm_args(fn, offsets, ws, dy=dy, x=x)
-    _need(fn, dy.dim() == 2 and x.dim() == 2 and dy.shape[0] == x.shape[0], "dy [rows, out], x [rows, in]")
+    sy, sx = dy.shape, x.shape
+    dev = _mm_check(fn, dy, x, offsets, ws, len(sy) == 2 and len(sx) == 2 and sy[0] == sx[0],
+                    "dy [rows, out], x [rows, in]")
     dt = out_dtype or (out.dtype if out is not None else dy.dtype)
-    _need(fn, dt in (dy.dtype, torch.float32), "out_dtype: the tensors' type or float32")
-    _need(fn, not accumulate or out is not None, "accumulate needs out")
-    rows, n_out, n_in = dy.shape[0], dy.shape[1], x.shape[1]
-    dw = _mm_out(fn, out, (E, n_out, n_in), dt, dy)
-    with torch.cuda.device(dy.device):
-        _check(fn, lib.moe_grouped_mm_wgrad(_ptr(dy), _ptr(x), _ptr(offsets), rows, E, n_out, n_in, f16, _ptr(dw),
-                                            int(dt == torch.float32), int(bool(accumulate)), _ptr(ws), ws.numel(),
-                                            _stream()))
+    if dt is not torch.float32 and dt is not dy.dtype:
+        raise MoEError(f"{fn}: out_dtype is the tensors' type or float32", -1)
+    if accumulate and out is None:
+        raise MoEError(f"{fn}: accumulate needs out", -1)
+    E = offsets.numel() - 1
+    dw = _mm_out(fn, out, (E, sy[1], sx[1]), dt, dy)
+    _on(dev, fn, lib.moe_grouped_mm_wgrad, dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), sy[0], E, sy[1], sx[1],
+        dy.dtype is torch.float16, dw.data_ptr(), dt is torch.float32, bool(accumulate), ws.data_ptr(), ws.numel())
     return dw
 
 
@@ -390,14 +396,13 @@ def quantize_int4_g128(w):
 def quantize_int8(x):
     """Rows of x (bf16 or fp16 [rows, cols]) -> (codes int8 [rows, cols], scales fp32 [rows])."""
     fn = "moe_quantize_int8"
-    _need(fn, x.dim() == 2 and x.dtype in (torch.bfloat16, torch.float16) and x.is_cuda and x.is_contiguous(),
-          "x: contiguous bf16 or fp16 [rows, cols] on a CUDA device")
+    if not (x.dim() == 2 and x.dtype in (torch.bfloat16, torch.float16) and x.is_cuda and x.is_contiguous()):
+        raise MoEError(f"{fn}: x: contiguous bf16 or fp16 [rows, cols] on a CUDA device", -1)
     rows, cols = x.shape
-    codes = torch.empty(rows, cols, dtype=torch.int8, device=x.device)
-    scales = torch.empty(rows, dtype=torch.float32, device=x.device)
-    with torch.cuda.device(x.device):
-        _check(fn, lib.moe_quantize_int8(_ptr(x), rows, cols, int(x.dtype == torch.float16), _ptr(codes),
-                                         _ptr(scales), _stream()))
+    codes = x.new_empty((rows, cols), dtype=torch.int8)
+    scales = x.new_empty((rows,), dtype=torch.float32)
+    _on(x.get_device(), fn, lib.moe_quantize_int8, x.data_ptr(), rows, cols, x.dtype is torch.float16,
+        codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
