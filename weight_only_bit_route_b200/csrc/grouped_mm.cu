@@ -12,9 +12,9 @@
 // the other axis: A's shared-memory tile is then stored along M (rows of 64 input features, one per output
 // feature) and the MMA descriptor says so; nothing is transposed.
 //
-// A tile is (expert, 128 * CG features, up to NT rows).  A persistent CTA (or pair) takes every grid-th tile;
-// every role computes the same sequence from a table of the experts' first tiles in shared memory, so nothing is
-// handed out through the workspace.  Warp roles:
+// A tile is (expert, 128 * CG features, up to NT rows).  A persistent CTA (or pair) takes a fixed sequence of
+// them; every role computes it from a table of the experts' first tiles in shared memory, so nothing is handed out
+// through the workspace.  Warp roles:
 //   warps 0, 3 TMA producers of A and B.  A stage is SL slices of K = 128 bytes (64 elements of 16 bits, 128 of 8)
 //              of A and B, 128-byte swizzled; rows past the tensors' ends arrive as zeros, and so does K past its end on both sides.
 //   warp 1     issues the MMAs (in a pair: the first CTA's warp, for both) and commits each stage.
@@ -139,15 +139,40 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
 
     uint8_t* ring = smem + ((1024u - (g_smem(smem) & 1023u)) & 1023u);
     int4* tbl = reinterpret_cast<int4*>(ring + S * C::kStage);      // active experts: {expert, first tile, first row, rows}
+    constexpr bool kSort = CG == 2;                  // large batches: the experts' tiles from the most rows to the fewest
+    constexpr int PER = (kMaxE + MM_THREADS - 1) / MM_THREADS;
+    if constexpr (kSort) {
+        int* rows_of = reinterpret_cast<int*>(ring);                 // scratch until the copies start
+        const int pad = (a.E + 3) & ~3;
+        for (int e = tid; e < pad; e += MM_THREADS) {
+            int base = 0, n = 0;
+            if (e < a.E) mm_expert_rows(a.offsets, e, a.rows, a.status, base, n);
+            rows_of[e] = n;
+        }
+        __syncthreads();
+        for (int e = tid; e < a.E; e += MM_THREADS)
+            tbl[mm_rank(rows_of, a.E, e)] = make_int4(e, 0, min(max(a.offsets[e], 0), a.rows), rows_of[e]);
+        g_fence_proxy_async();                                       // before the copies write the scratch
+        __syncthreads();
+    }
     {
-        constexpr int PER = (kMaxE + MM_THREADS - 1) / MM_THREADS;
-        int eb[PER], ne[PER], nt[PER], local = 0, ltiles = 0;
+        int ex[PER], eb[PER], ne[PER], nt[PER], local = 0, ltiles = 0;
 #pragma unroll
         for (int i = 0; i < PER; i++) {
             const int e = tid * PER + i;
+            ex[i] = e;
             eb[i] = 0;
             ne[i] = 0;
-            if (e < a.E) mm_expert_rows(a.offsets, e, a.rows, a.status, eb[i], ne[i]);
+            if (e < a.E) {
+                if constexpr (kSort) {
+                    const int4 te = tbl[e];
+                    ex[i] = te.x;
+                    eb[i] = te.z;
+                    ne[i] = te.w;
+                } else {
+                    mm_expert_rows(a.offsets, e, a.rows, a.status, eb[i], ne[i]);
+                }
+            }
             nt[i] = ((ne[i] + NT - 1) / NT) * MT;
             local += ne[i] > 0;
             ltiles += nt[i];
@@ -168,7 +193,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
         int pos = base + v - local, tpos = tbase + w - ltiles;
 #pragma unroll
         for (int i = 0; i < PER; i++)
-            if (ne[i] > 0) { tbl[pos] = make_int4(tid * PER + i, tpos, eb[i], ne[i]); pos++; tpos += nt[i]; }
+            if (ne[i] > 0) { tbl[pos] = make_int4(ex[i], tpos, eb[i], ne[i]); pos++; tpos += nt[i]; }
         if (tid == 0) { s_nact = tot; s_total = ttot; }
     }
     g_fence_before();
@@ -177,8 +202,8 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
     g_fence_after();
 
     const uint32_t tmem = s_tmem;
-    const int ntiles = s_total, nact = s_nact;
-    const int tile0 = int(blockIdx.x) / CG, tstep = int(gridDim.x) / CG;
+    const int nact = s_nact;
+    const MmSequence seq(int(blockIdx.x) / CG, int(gridDim.x) / CG, s_total, kSort);
     auto tile_of = [&](int tile) {
         int lo = 0, hi = nact - 1;
         while (lo < hi) {
@@ -212,8 +237,8 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
         if (isb && a.early) asm volatile("griddepcontrol.wait;" ::: "memory");      // the row pass's output
         uint32_t it = 0;
         bool ok = true;
-        for (int tile = tile0; tile < ntiles && ok && !g_aborted(&s_ab); tile += tstep) {
-            const MmTile T = tile_of(tile);
+        for (int i = 0; i < seq.count && ok && !g_aborted(&s_ab); i++) {
+            const MmTile T = tile_of(seq.tile(i));
             const int half = T.bn / CG;                            // rows of B this CTA stages
             // the smallest box that holds them (the rows too many are never multiplied)
             const int bx = half <= 16 ? 0 : half <= 32 ? 1 : half <= 64 ? 2 : 3;
@@ -282,8 +307,8 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
         uint32_t it = 0;
         MmHalves acc;
         bool ok = true;
-        for (int tile = tile0; tile < ntiles && ok && !g_aborted(&s_ab); tile += tstep) {
-            const MmTile T = tile_of(tile);
+        for (int i = 0; i < seq.count && ok && !g_aborted(&s_ab); i++) {
+            const MmTile T = tile_of(seq.tile(i));
             const uint32_t idesc = I8 ? g_idesc_s8(T.bn, 128 * CG)
                                       : (g_idesc(T.bn, a.f16 != 0, 128 * CG) | (AMN ? G_IDESC_A_MN : 0u));
             const bool both = T.bn > C::kHalfRows;
@@ -349,8 +374,8 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
         constexpr int kScaleRegs = I8 ? (NT + 63) / 64 : 1;
         MmHalves use;
         bool ok = true;
-        for (int tile = tile0; tile < ntiles && !g_aborted(&s_ab); tile += tstep) {
-            const MmTile T = tile_of(tile);
+        for (int ti = 0; ti < seq.count && !g_aborted(&s_ab); ti++) {
+            const MmTile T = tile_of(seq.tile(ti));
             const int m = T.m0 + int(rank) * 128 + q * 32 + lane;            // my feature
             const bool mine = m < a.mdim;
             float w0 = 0.f, w1 = 0.f;

@@ -16,6 +16,37 @@ __device__ __forceinline__ void mm_expert_rows(const int32_t* offsets, int e, in
     if (base != o0 || end != o1) set_status(status, MOE_ERR_DEVICE_INDEX);
 }
 
+// The tiles of worker p of P, as a sequence: tile p of each round of P, in snake order (every second round runs
+// backwards) where the tiles are listed from the largest to the smallest, so that the workers' sums stay within
+// about one small tile of each other; the upper half of the workers then starts from the small end, so that
+// compute-bound and memory-bound tiles run at the same time.
+struct MmSequence {
+    int p, P, count;
+    bool snake;
+    __device__ __forceinline__ MmSequence(int p_, int P_, int ntiles, bool snake_) : p(p_), P(P_), snake(snake_) {
+        const int full = ntiles / P, rem = ntiles - full * P;
+        count = full + (at(full) < rem ? 1 : 0);
+    }
+    __device__ __forceinline__ int at(int round) const { return snake && (round & 1) ? P - 1 - p : p; }
+    __device__ __forceinline__ int tile(int i) const {
+        const int round = snake && p >= P / 2 ? count - 1 - i : i;
+        return round * P + at(round);
+    }
+};
+
+// Position of expert e among the experts by rows, most first (n: rows of the E experts in shared memory, zeros up to
+// the next multiple of 4).
+__device__ __forceinline__ int mm_rank(const int* n, int E, int e) {
+    const int mine = n[e];
+    int r = 0;
+    for (int i = 0; i < E; i += 4) {
+        const int4 v = *reinterpret_cast<const int4*>(n + i);
+        r += (v.x > mine || (v.x == mine && i < e)) + (v.y > mine || (v.y == mine && i + 1 < e)) +
+             (v.z > mine || (v.z == mine && i + 2 < e)) + (v.w > mine || (v.w == mine && i + 3 < e));
+    }
+    return r;
+}
+
 struct MmProblem {
     const void* act;             // rows of the contraction: x or codes [rows, in], dy [rows, out] (grad)
     const void* w0; const void* w1;      // weights [E, out, in]; w1: up (int8 gate/up), else null
