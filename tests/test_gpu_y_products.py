@@ -103,6 +103,26 @@ def test_products_match_the_formula(load, K, N, dtype):
         assert ((acc[e].double() - ref).abs() <= bound).all(), ("accumulated", e)
 
 
+@pytest.mark.parametrize("K,N", [(4096, 136), (2056, 392), (1024, 1000), (320, 64)])
+@pytest.mark.parametrize("counts", [[3], [61], [1, 0, 16, 17], [64], [40, 64, 3]], ids=str)
+def test_few_tiles_share_a_long_contraction(counts, K, N):
+    """Few tiles: clusters split the contraction (of K forward, of N in the gradient), and the parts are joined."""
+    E, rows = len(counts), sum(counts) + 5
+    g = gen(20)
+    x, dy, w = normal(g, rows, K), normal(g, rows, N), normal(g, E, N, K, std=0.1)
+    wt = w.transpose(1, 2).contiguous()
+    off, ws = offsets_of(counts), moe.control_block()
+    y, dx = moe.grouped_mm(x, w, off, ws), moe.grouped_mm_dgrad(x, wt, off, ws)
+    assert moe.read_status(ws) == 0
+    for e, a, b in spans(counts):
+        xe, we = x[a:b].double(), w[e].double()
+        ref, mag = xe @ we.T, xe.abs() @ we.abs().T
+        for got in (y, dx):                      # dx by the transposed weights is the same product
+            assert ((got[a:b].double() - ref).abs() <= product_bound(mag, K, ref, torch.bfloat16)).all(), e
+    for _ in range(2):
+        assert torch.equal(moe.grouped_mm(x, w, off, ws)[:sum(counts)], y[:sum(counts)])
+
+
 def test_an_expert_keeps_its_infinities():
     """Inf and NaN in one expert's rows or weights reach only that expert's results."""
     counts = [5, 19, 30]
@@ -257,11 +277,12 @@ COUNTS8 = {
     "decode": ([1, 0, 2, 1, 0, 0, 4, 1, 1, 6], 8),
     "big": ([600, 0, 257, 7], 8),
     "single": ([37], 1),
+    "pair": ([61, 3], 2),
 }
 
 
 @pytest.mark.parametrize("load", list(COUNTS8))
-@pytest.mark.parametrize("H,F", [(256, 128), (1024, 384), (640, 256)])
+@pytest.mark.parametrize("H,F", [(256, 128), (1024, 384), (640, 256), (4096, 1152)])
 def test_int8_steps_match_the_formula(load, H, F):
     counts, k = COUNTS8[load]
     E, rows = len(counts), sum(counts)
@@ -483,8 +504,29 @@ def test_two_streams_and_threads():
             assert torch.equal(a, b)
 
 
-def test_wait_limit_runs_out_then_recovers():
-    run, new_ws = _calls()
+def _large_calls():
+    """The same calls at sizes that run on CTA pairs, and with few tiles on clusters that share a contraction."""
+    counts, few, k, H, F = [700, 0, 300, 24], [3, 60], 8, 512, 256
+    g = gen(16)
+    rows = sum(counts)
+    x, dy, w = normal(g, rows, 520), normal(g, rows, 392), normal(g, 4, 392, 520)
+    xs, ws_ = normal(g, 63, 2048), normal(g, 2, 136, 2048)
+    off, offs, rs = offsets_of(counts), offsets_of(few), routing(counts, k, g)
+    x8 = normal(g, rows // k, H)
+    gate, up, down = int8_bank(g, 4, F, H), int8_bank(g, 4, F, H), int8_bank(g, 4, H, F)
+
+    def run(ws):
+        h = moe.grouped_swiglu(x8, off, rs, k, gate, up, rows, ws)
+        return [moe.grouped_mm(x, w, off, ws), moe.grouped_mm_dgrad(dy, w, off, ws), moe.grouped_mm_wgrad(dy, x, off, ws),
+                moe.grouped_mm_wgrad(dy, x, off, ws, out_dtype=torch.float32), moe.grouped_mm(xs, ws_, offs, ws), h,
+                moe.grouped_down(h, off, rs, None, down, ws)]
+
+    return run, lambda: moe.workspace(rows // k, H, 4, F, 4)
+
+
+@pytest.mark.parametrize("calls", [_calls, _large_calls], ids=["small", "large"])
+def test_wait_limit_runs_out_then_recovers(calls):
+    run, new_ws = calls()
     ws = new_ws()
     ref = run(ws)
     assert moe.read_status(ws) == 0

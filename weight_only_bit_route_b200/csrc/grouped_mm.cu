@@ -24,6 +24,7 @@
 //
 // Every wait is bounded (moe_set_wait_limit).  On expiry the kernel records MOE_ERR_TIMEOUT, stops issuing work,
 // waits (bounded) for its copies and MMAs in flight, frees its tensor memory and returns.
+#include <algorithm>
 #include <cstring>
 
 #include "grouped_mm.cuh"
@@ -35,8 +36,9 @@ constexpr int MM_THREADS = 384;
 constexpr int MM_EPI_WARPS = 8;
 constexpr int MM_BOXES = 4;
 
-// Tile shape of one instantiation.  NT: rows per tile; CG: CTAs per tile; SL: 128-byte slices of K per stage.
-template <bool I8, bool AMN, bool GU, int NT, int CG, int SL>
+// Tile shape of one instantiation.  NT: rows per tile; CG: CTAs per tile; SL: 128-byte slices of K per stage; SPLIT:
+// a cluster shares a tile's K.
+template <bool I8, bool AMN, bool GU, int NT, int CG, int SL, bool SPLIT>
 struct MmCfg {
     static constexpr int kMat = GU ? 2 : 1;
     static constexpr int kBK = (I8 ? 128 : 64) * SL;              // K per stage
@@ -44,8 +46,12 @@ struct MmCfg {
     static constexpr int kABytes = SL * 128 * 128;                // per matrix
     static constexpr int kBBytes = SL * NT / CG * 128;
     static constexpr int kStage = kMat * kABytes + kBBytes;
-    static constexpr int kRingBytes = 200 * 1024;                 // beside it: the tile table (16 bytes per expert)
+    // split K: partial sums from the other CTAs, 8 KB per block of 16 rows and matrix
+    static constexpr int kMaxSplit = GU ? 4 : 8;
+    static constexpr int kRedBytes = SPLIT ? (kMaxSplit - 1) * kMat * 8192 : 0;      // (z - 1) ceil(NT / 16 / z) <= kMaxSplit - 1
+    static constexpr int kRingBytes = 200 * 1024 - kRedBytes;     // beside them: the tile table (16 bytes per expert)
     static constexpr int kStages = kRingBytes / kStage < 12 ? kRingBytes / kStage : 12;
+    static constexpr int kBlocks = NT / 16;
     static constexpr int kAccCols = kMat * NT;                    // one accumulator buffer
     // Accumulators take tensor memory in two halves, in turn; a tile of more than kHalfRows rows takes both.
     static constexpr int kHalfRows = 2 * kAccCols <= 512 ? NT : NT / 2;
@@ -54,6 +60,7 @@ struct MmCfg {
     static constexpr int kTmem = kTmemCols <= 32 ? 32 : (kTmemCols <= 64 ? 64 : (kTmemCols <= 128 ? 128 : (kTmemCols <= 256 ? 256 : 512)));
     static constexpr int kStep = 16 * CG;                         // a tile's N is a multiple of this
     static_assert(kAccCols <= 512 && NT % kStep == 0 && kStages >= 2, "tile shape");
+    static_assert(!SPLIT || (CG == 1 && NT <= 64), "split K: the partial sums fit");
     static_assert(NT / CG <= (16 << (MM_BOXES - 1)), "the largest box holds a tile's rows");
 };
 
@@ -83,6 +90,8 @@ struct MmArgs {
     int E, mdim, kdim, rows;             // mdim: output features (A's M), kdim: contraction length
     int f16;                             // 16-bit elements are fp16 (else bf16)
     int chunked;                         // bit 0: a0 and a1, bit 1: b see K (gradient: A's features) in 128-byte chunks
+    int split_tiles;                     // split K: clusters to launch, if they fit
+    int split;                           // CTAs that share a tile's K (1: none)
     int early;                           // the kernel before is this product's own row pass
 };
 
@@ -99,12 +108,36 @@ __device__ __forceinline__ void mm_copy4(uint32_t dst, const CUtensorMap* map, i
     if (CG == 2) g_tma4d_pair(dst, map, x, y, z, w, bar); else g_tma4d(dst, map, x, y, z, w, bar);
 }
 
-template <bool I8, bool AMN, bool GU, int NT, int CG, int SL>
+// The sum of a lane's 16 columns over the z CTAs that share a tile's K, in the order of the CTAs (own: v)
+template <bool I8>
+__device__ __forceinline__ void mm_join(uint32_t (&v)[16], const uint8_t* red, int stride, int z, uint32_t krank, int row) {
+    uint32_t sum[16];
+#pragma unroll
+    for (int j = 0; j < 16; j++) sum[j] = 0;                       // (0 is zero in both types)
+    for (int r = 0; r < z; r++) {
+        const bool own = r == int(krank);
+        const uint8_t* p = red + (r < int(krank) ? r : r - 1) * stride + row * 16;
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            uint4 o = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            if (!own) o = *reinterpret_cast<const uint4*>(p + j * 2048);
+            const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                sum[4 * j + i] = I8 ? sum[4 * j + i] + w[i]
+                                    : __float_as_uint(__uint_as_float(sum[4 * j + i]) + __uint_as_float(w[i]));
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 16; j++) v[j] = sum[j];
+}
+
+template <bool I8, bool AMN, bool GU, int NT, int CG, int SL, bool SPLIT>
 __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant__ MmArgs a) {
-    using C = MmCfg<I8, AMN, GU, NT, CG, SL>;
+    using C = MmCfg<I8, AMN, GU, NT, CG, SL, SPLIT>;
     constexpr int S = C::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ __align__(8) uint64_t full[S], empty[S], acc_full[2], acc_empty[2], drain, hold_bar;
+    __shared__ __align__(8) uint64_t full[S], empty[S], acc_full[2], acc_empty[2], drain, hold_bar, red_full, red_free;
     __shared__ uint32_t s_tmem;
     __shared__ uint32_t s_issued[2];                 // stages this CTA's two producers have issued
     __shared__ int s_wsum[MM_THREADS / 32], s_wt[MM_THREADS / 32], s_nact, s_total, s_hold;
@@ -114,7 +147,11 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
     const uint32_t rank = CG == 2 ? g_cta_rank() : 0u;
     const int MT = (a.mdim + 128 * CG - 1) / (128 * CG);
     const int KS = (a.kdim + C::kBK - 1) / C::kBK;
+    const int z = SPLIT ? a.split : 1;
+    const uint32_t krank = SPLIT ? g_cta_rank() : 0u;
+    const int kper = (KS + z - 1) / z, ks0 = int(krank) * kper, ks1 = min(KS, ks0 + kper);      // this CTA's stages of K
 
+    if (warp == 4 && lane < 2) g_prefetch_map(lane ? &a.b[0] : &a.a0);
     if (tid == 0) {
         for (int s = 0; s < S; s++) {
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(g_smem(&full[s])), "r"(2 * CG));
@@ -126,19 +163,24 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
         }
         asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(g_smem(&drain)));
         asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(g_smem(&hold_bar)));
+        if (SPLIT) {
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(g_smem(&red_full)), "r"((z - 1) * MM_EPI_WARPS));
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(g_smem(&red_free)), "r"((z - 1) * MM_EPI_WARPS));
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         s_ab.flag = 0;
         s_issued[0] = s_issued[1] = 0;
     }
     if (warp == 2) g_tmem_alloc<CG>(g_smem(&s_tmem), C::kTmem);
     if (!a.early) asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (tid == 0) {
+    if (tid == MM_THREADS - 1) {                     // (a thread with few offsets or none to wait for)
         s_ab.limit_ns = g_limit_from(a.status);
         s_hold = g_hold_from(a.status);
     }
 
     uint8_t* ring = smem + ((1024u - (g_smem(smem) & 1023u)) & 1023u);
-    int4* tbl = reinterpret_cast<int4*>(ring + S * C::kStage);      // active experts: {expert, first tile, first row, rows}
+    uint8_t* red = ring + S * C::kStage;             // split K: [other CTA][own block][matrix][4][128 lanes] of 16 bytes
+    int4* tbl = reinterpret_cast<int4*>(red + C::kRedBytes);        // active experts: {expert, first tile, first row, rows}
     constexpr bool kSort = CG == 2;                  // large batches: the experts' tiles from the most rows to the fewest
     constexpr int PER = (kMaxE + MM_THREADS - 1) / MM_THREADS;
     if constexpr (kSort) {
@@ -198,12 +240,13 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
     }
     g_fence_before();
     __syncthreads();
-    if (CG == 2) g_cluster_sync();                   // the other CTA's barriers exist before anything arrives there
+    if (CG == 2 || SPLIT) g_cluster_sync();          // the other CTAs' barriers exist before anything arrives there
     g_fence_after();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (they wait for this kernel's end themselves)
 
     const uint32_t tmem = s_tmem;
     const int nact = s_nact;
-    const MmSequence seq(int(blockIdx.x) / CG, int(gridDim.x) / CG, s_total, kSort);
+    const MmSequence seq(int(blockIdx.x) / (CG * z), int(gridDim.x) / (CG * z), s_total, kSort);
     auto tile_of = [&](int tile) {
         int lo = 0, hi = nact - 1;
         while (lo < hi) {
@@ -245,7 +288,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
             const uint32_t slice = uint32_t(16 << bx) * 128u;
             const uint32_t bytes = isb ? SL * slice : uint32_t(C::kMat * C::kABytes);
             const int r0 = T.n0 + int(rank) * half, m0 = T.m0 + int(rank) * 128;
-            for (int ks = 0; ks < KS; ks++, it++) {
+            for (int ks = ks0; ks < ks1; ks++, it++) {
                 const int s = it % S;
                 if (it >= uint32_t(S) && !g_wait_w(g_smem(&empty[s]), ((it / S) - 1) & 1, &s_ab, 32)) {
                     ok = false;
@@ -323,7 +366,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
             }
             acc.take(h, both);
             g_fence_after();
-            for (int ks = 0; ks < KS; ks++, it++) {
+            for (int ks = ks0; ks < ks1; ks++, it++) {
                 const int s = it % S;
                 if (!g_wait_w(g_smem(&full[s]), (it / S) & 1, &s_ab)) {
                     ok = false;
@@ -337,7 +380,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
                     for (int k = 0; k < 4 * SL; k++) {
                         if (k >= steps) break;                     // K ends here
                         const uint64_t bd = g_desc(sb + (k / 4) * slice + (k % 4) * 32);
-                        const uint32_t add = (k > 0 || ks > 0) ? 1u : 0u;
+                        const uint32_t add = (k > 0 || ks > ks0) ? 1u : 0u;
 #pragma unroll
                         for (int m = 0; m < C::kMat; m++) {
                             const uint32_t am = sa + m * C::kABytes;
@@ -348,7 +391,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
                         }
                     }
                     g_commit_cg<CG>(g_smem(&empty[s]));
-                    if (ks == KS - 1) {
+                    if (ks == ks1 - 1) {
                         g_commit_cg<CG>(g_smem(&acc_full[h]));
                         if (both) g_commit_cg<CG>(g_smem(&acc_full[1]));
                     }
@@ -410,14 +453,53 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
             g_fence_after();
             const uint32_t acc = tmem + lane_addr + h * C::kHalfCols, up = both ? NT : C::kHalfRows;
             uint16_t* dst = a.out + size_t(T.n0 + odd) * a.mdim + (m - odd);
+            if constexpr (SPLIT) {
+                // Block b of 16 rows is summed by CTA b mod z: hand it the others' partial sums, then wait for theirs.
+                if (ti > 0 && !g_wait_w(g_smem(&red_free), (ti - 1) & 1, &s_ab, 32)) {
+                    ok = false;
+                    break;
+                }
+                for (int b = hsel; b * 16 < T.nval; b += 2) {
+                    const uint32_t own = uint32_t(b) & (z - 1);
+                    if (own == krank) continue;
+                    const uint32_t slot = krank < own ? krank : krank - 1;
+                    const uint32_t to = g_mapa(g_smem(red), own) + ((slot * (C::kBlocks / z + (C::kBlocks < z)) + uint32_t(b) / z) * C::kMat) * 8192 +
+                                        uint32_t(q * 32 + lane) * 16;
+#pragma unroll
+                    for (int mat = 0; mat < C::kMat; mat++) {
+                        uint32_t v[16];
+                        g_ld16(acc + mat * up + b * 16, v);
+                        g_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 4; j++)
+                            g_st_cluster4(to + mat * 8192 + j * 2048, v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    }
+                }
+                g_fence_cluster();
+                __syncwarp();
+                if (lane < z && lane != int(krank)) g_arrive_remote(g_mapa(g_smem(&red_full), lane));
+                if (!g_wait_w(g_smem(&red_full), ti & 1, &s_ab, 32)) {
+                    ok = false;
+                    break;
+                }
+                g_fence_cluster();
+            }
 #pragma unroll
             for (int i = 0; i < (NT + 31) / 32; i++) {
                 const int c = (2 * i + hsel) * 16;
                 if (c >= T.nval) break;
+                if (SPLIT && (uint32_t(c / 16) & (z - 1)) != krank) continue;
                 uint32_t v[16], u[16];
                 g_ld16(acc + c, v);
                 if constexpr (GU) g_ld16(acc + up + c, u);
                 g_ld_wait();
+                if constexpr (SPLIT) {
+                    mm_join<I8>(v, red + (c / 16 / z) * (C::kMat * 8192), C::kMat * 8192 * (C::kBlocks / z + (C::kBlocks < z)),
+                                z, krank, q * 32 + lane);
+                    if constexpr (GU)
+                        mm_join<I8>(u, red + (c / 16 / z) * (C::kMat * 8192) + 8192,
+                                    C::kMat * 8192 * (C::kBlocks / z + (C::kBlocks < z)), z, krank, q * 32 + lane);
+                }
                 float y[16];
 #pragma unroll
                 for (int j = 0; j < 16; j++) {
@@ -457,16 +539,17 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
                 }
             }
             use.take(h, both);
+            if (SPLIT && ti + 1 < seq.count && lane < z && lane != int(krank)) g_arrive_remote(g_mapa(g_smem(&red_free), lane));
         }
         if (!ok) fail();
     }
 
     g_fence_before();
     __syncthreads();
-    if (CG == 2) g_cluster_sync();
+    if (CG == 2 || SPLIT) g_cluster_sync();
     // after an expired wait, copies may be in flight for a stage that only some producers had issued: stand in for
     // the others' arrivals, then wait (bounded) for the last stages
-    if (rank == 0 && tid == 0) {
+    if (rank == 0 && tid == 0 && (CG == 2 || s_ab.flag)) {
         uint32_t n_[2 * CG], hi = 0;
         for (int i = 0; i < 2 * CG; i++) {
             n_[i] = i < 2 ? s_issued[i] : g_ld_cluster(g_mapa(g_smem(&s_issued[i & 1]), 1));
@@ -488,21 +571,36 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-template <bool I8, bool AMN, bool GU, int NT, int CG, int SL>
+template <bool I8, bool AMN, bool GU, int NT, int CG, int SL, bool SPLIT>
 static int mm_launch(const MmArgs& a, cudaStream_t s) {
-    using C = MmCfg<I8, AMN, GU, NT, CG, SL>;
-    auto k = mm_kernel<I8, AMN, GU, NT, CG, SL>;
-    constexpr int kSmem = C::kStages * C::kStage + 1024 + 16 * kMaxE;
+    using C = MmCfg<I8, AMN, GU, NT, CG, SL, SPLIT>;
+    auto k = mm_kernel<I8, AMN, GU, NT, CG, SL, SPLIT>;
+    constexpr int kFixed = C::kStages * C::kStage + C::kRedBytes + 1024;
+    constexpr int kSmem = kFixed + 16 * kMaxE;
     int sms = 0;
     const int rc = mm_kernel_ready(reinterpret_cast<const void*>(k), kSmem, &sms);
     if (rc != MOE_OK) return rc;
-    const int smem = C::kStages * C::kStage + 1024 + 16 * a.E;
-    return mm_launch_cfg(k, dim3(sms / CG * CG), dim3(MM_THREADS), smem, CG, s, a);
+    // (clusters of 4 or 8: the tiles' own number, since not every SM can hold one)
+    const int cl = SPLIT ? a.split : CG, grid = SPLIT ? std::max(1, std::min(a.split_tiles, sms / cl)) * cl : sms / cl * cl;
+    return mm_launch_cfg(k, dim3(grid), dim3(MM_THREADS), kFixed + 16 * a.E, cl, s, a);
 }
 
 // Tile shape by the average number of rows per expert: 0 (16 rows), 1 (64), 2 (256, a CTA pair).
 static int mm_shape(const MmProblem& p) { return p.rows <= 16 * p.E ? 0 : p.rows <= 64 * p.E ? 1 : 2; }
 static int mm_slices(const MmProblem& p) { return mm_shape(p) == 0 || p.w1 ? 1 : 2; }
+// Few tiles leave SMs idle: then clusters of 2, 4 or 8 CTAs (gate/up: 4 at most) share each tile's K, as many as give
+// every SM a CTA, while each still has two stages of K.  *tiles: about how many tiles there are.
+static int mm_split(const MmProblem& p, int shape, int* tiles) {
+    const int nt = shape ? 64 : 16, mdim = p.grad ? p.in_dim : p.out_dim, kdim = p.grad ? p.out_dim : p.in_dim;
+    const int64_t rowtiles = std::max(std::min(p.E, p.rows), (p.rows + nt - 1) / nt);
+    const int64_t t = rowtiles * ((mdim + 127) / 128);
+    const int bk = (p.i8 ? 128 : 64) * mm_slices(p), ks = (kdim + bk - 1) / bk;
+    int z = 1;
+    if (shape < 2)
+        while (z < (p.w1 ? 4 : 8) && t * 2 * z <= 148 && ks >= 4 * z && int64_t(2 * z - 1) * ((ks + 2 * z - 1) / (2 * z)) < ks) z *= 2;
+    *tiles = int(std::min<int64_t>(t, 1 << 20));
+    return z;
+}
 
 static CUtensorMapDataType mm_type(bool i8, bool f16) {
     return i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : (f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
@@ -552,17 +650,24 @@ int launch_grouped_mm(const MmProblem& p, cudaStream_t s) {
     a.rows = p.rows;
     a.f16 = p.f16;
     a.early = p.i8;
-    switch (mm_shape(p)) {
-        case 0:
-            if (p.i8) return p.w1 ? mm_launch<true, false, true, 16, 1, 1>(a, s) : mm_launch<true, false, false, 16, 1, 1>(a, s);
-            return p.grad ? mm_launch<false, true, false, 16, 1, 1>(a, s) : mm_launch<false, false, false, 16, 1, 1>(a, s);
-        case 1:
-            if (p.i8) return p.w1 ? mm_launch<true, false, true, 64, 1, 1>(a, s) : mm_launch<true, false, false, 64, 1, 2>(a, s);
-            return p.grad ? mm_launch<false, true, false, 64, 1, 2>(a, s) : mm_launch<false, false, false, 64, 1, 2>(a, s);
-        default:
-            if (p.i8) return p.w1 ? mm_launch<true, false, true, 256, 2, 1>(a, s) : mm_launch<true, false, false, 256, 2, 2>(a, s);
-            return p.grad ? mm_launch<false, true, false, 256, 2, 2>(a, s) : mm_launch<false, false, false, 256, 2, 2>(a, s);
+    const int shape = mm_shape(p);
+    a.split = mm_split(p, shape, &a.split_tiles);
+    if (a.split > 1) {
+        if (p.i8 && p.w1) return shape ? mm_launch<true, false, true, 64, 1, 1, true>(a, s) : mm_launch<true, false, true, 16, 1, 1, true>(a, s);
+        if (p.i8) return shape ? mm_launch<true, false, false, 64, 1, 2, true>(a, s) : mm_launch<true, false, false, 16, 1, 1, true>(a, s);
+        if (p.grad) return shape ? mm_launch<false, true, false, 64, 1, 2, true>(a, s) : mm_launch<false, true, false, 16, 1, 1, true>(a, s);
+        return shape ? mm_launch<false, false, false, 64, 1, 2, true>(a, s) : mm_launch<false, false, false, 16, 1, 1, true>(a, s);
     }
+    if (shape == 0) {
+        if (p.i8) return p.w1 ? mm_launch<true, false, true, 16, 1, 1, false>(a, s) : mm_launch<true, false, false, 16, 1, 1, false>(a, s);
+        return p.grad ? mm_launch<false, true, false, 16, 1, 1, false>(a, s) : mm_launch<false, false, false, 16, 1, 1, false>(a, s);
+    }
+    if (shape == 1) {
+        if (p.i8) return p.w1 ? mm_launch<true, false, true, 64, 1, 1, false>(a, s) : mm_launch<true, false, false, 64, 1, 2, false>(a, s);
+        return p.grad ? mm_launch<false, true, false, 64, 1, 2, false>(a, s) : mm_launch<false, false, false, 64, 1, 2, false>(a, s);
+    }
+    if (p.i8) return p.w1 ? mm_launch<true, false, true, 256, 2, 1, false>(a, s) : mm_launch<true, false, false, 256, 2, 2, false>(a, s);
+    return p.grad ? mm_launch<false, true, false, 256, 2, 2, false>(a, s) : mm_launch<false, false, false, 256, 2, 2, false>(a, s);
 }
 
 }  // namespace moe
