@@ -53,6 +53,8 @@ def product_bound(mag, K, ref, dtype):
 
 
 COUNTS = {
+    "many": [1100, 0],
+    "long": [2049],
     "ragged": [0, 1, 16, 17, 0, 63, 64, 65, 255, 0],
     "one_each": [1] * 9,
     "big": [600, 0, 257, 5],

@@ -585,19 +585,29 @@ static int mm_launch(const MmArgs& a, cudaStream_t s) {
     return mm_launch_cfg(k, dim3(grid), dim3(MM_THREADS), kFixed + 16 * a.E, cl, s, a);
 }
 
-// Tile shape by the average number of rows per expert: 0 (16 rows), 1 (64), 2 (256, a CTA pair).
-static int mm_shape(const MmProblem& p) { return p.rows <= 16 * p.E ? 0 : p.rows <= 64 * p.E ? 1 : 2; }
-static int mm_slices(const MmProblem& p) { return mm_shape(p) == 0 || p.w1 ? 1 : 2; }
+static int mm_mdim(const MmProblem& p) { return p.grad ? p.in_dim : p.out_dim; }
+// About how many (expert, row block) pairs there are with blocks of nt rows
+static int64_t mm_row_blocks(const MmProblem& p, int nt) { return std::max(std::min(p.E, p.rows), (p.rows + nt - 1) / nt); }
+
+// Tiles of 256 rows x 256 features on CTA pairs when the experts hold more than 64 rows on average and half the pairs
+// get a tile; else 64 rows x 128 features on single CTAs.  Measured (4096 -> 1536, us, single / pair): 352 experts of
+// 47 rows 682 / 725 in bf16, 712 / 694 in int8 gate/up; 44 experts of 1490 rows 1122 / 629; one expert of 300 rows
+// 14 / 20, of 1000 rows (24 pair tiles) 30 / 27, of 3000 57 / 29; four of 150 rows (24 pair tiles, K 2048) 11 / 14.
+// (Tiles of 16 rows were never faster than those of 64: 8 tokens over 352 experts 121 us against 117.)
+static bool mm_pair(const MmProblem& p) {
+    return p.rows > 64 * int64_t(p.E) && mm_row_blocks(p, 256) * ((mm_mdim(p) + 255) / 256) >= 37;
+}
+// K slices per stage: two where the stage then still fits the ring four times
+static int mm_slices(const MmProblem& p) { return p.w1 ? 1 : 2; }
 // Few tiles leave SMs idle: then clusters of 2, 4 or 8 CTAs (gate/up: 4 at most) share each tile's K, as many as give
-// every SM a CTA, while each still has two stages of K.  *tiles: about how many tiles there are.
-static int mm_split(const MmProblem& p, int shape, int* tiles) {
-    const int nt = shape ? 64 : 16, mdim = p.grad ? p.in_dim : p.out_dim, kdim = p.grad ? p.out_dim : p.in_dim;
-    const int64_t rowtiles = std::max(std::min(p.E, p.rows), (p.rows + nt - 1) / nt);
-    const int64_t t = rowtiles * ((mdim + 127) / 128);
+// every SM a CTA, while each still has two stages of K (one expert, 4096 -> 1536: 8 rows 18 us without, 9 with; int8
+// gate/up of 61 rows 18 / 13).
+static int mm_split(const MmProblem& p, int* tiles) {
+    const int kdim = p.grad ? p.out_dim : p.in_dim;
+    const int64_t t = mm_row_blocks(p, 64) * ((mm_mdim(p) + 127) / 128);
     const int bk = (p.i8 ? 128 : 64) * mm_slices(p), ks = (kdim + bk - 1) / bk;
     int z = 1;
-    if (shape < 2)
-        while (z < (p.w1 ? 4 : 8) && t * 2 * z <= 148 && ks >= 4 * z && int64_t(2 * z - 1) * ((ks + 2 * z - 1) / (2 * z)) < ks) z *= 2;
+    while (z < (p.w1 ? 4 : 8) && t * 2 * z <= 148 && ks >= 4 * z && int64_t(2 * z - 1) * ((ks + 2 * z - 1) / (2 * z)) < ks) z *= 2;
     *tiles = int(std::min<int64_t>(t, 1 << 20));
     return z;
 }
@@ -630,7 +640,8 @@ int launch_grouped_mm(const MmProblem& p, cudaStream_t s) {
         rc = ca ? g_map4(map, ty, w, bi, p.out_dim, p.in_dim / bk, p.E, pitch, zp, br)
                 : g_map3(map, ty, w, p.in_dim, p.out_dim, p.E, pitch, zp, bi, br);
     }
-    const int boxes = mm_shape(p) == 0 ? 1 : mm_shape(p) == 1 ? 3 : MM_BOXES;     // those a tile of this shape can ask for
+    const bool pair = mm_pair(p);
+    const int boxes = pair ? MM_BOXES : 3;                // those a tile of this shape can ask for
     for (int i = 0; i < boxes && rc == MOE_OK; i++)
         rc = cb ? g_map4(&a.b[i], ty, p.act, bk, p.rows, kdim / bk, 1, uint64_t(kdim) * el, uint64_t(kdim) * el * p.rows,
                          16u << i)
@@ -650,24 +661,17 @@ int launch_grouped_mm(const MmProblem& p, cudaStream_t s) {
     a.rows = p.rows;
     a.f16 = p.f16;
     a.early = p.i8;
-    const int shape = mm_shape(p);
-    a.split = mm_split(p, shape, &a.split_tiles);
+    if (pair) {
+        if (p.i8) return p.w1 ? mm_launch<true, false, true, 256, 2, 1, false>(a, s) : mm_launch<true, false, false, 256, 2, 2, false>(a, s);
+        return p.grad ? mm_launch<false, true, false, 256, 2, 2, false>(a, s) : mm_launch<false, false, false, 256, 2, 2, false>(a, s);
+    }
+    a.split = mm_split(p, &a.split_tiles);
     if (a.split > 1) {
-        if (p.i8 && p.w1) return shape ? mm_launch<true, false, true, 64, 1, 1, true>(a, s) : mm_launch<true, false, true, 16, 1, 1, true>(a, s);
-        if (p.i8) return shape ? mm_launch<true, false, false, 64, 1, 2, true>(a, s) : mm_launch<true, false, false, 16, 1, 1, true>(a, s);
-        if (p.grad) return shape ? mm_launch<false, true, false, 64, 1, 2, true>(a, s) : mm_launch<false, true, false, 16, 1, 1, true>(a, s);
-        return shape ? mm_launch<false, false, false, 64, 1, 2, true>(a, s) : mm_launch<false, false, false, 16, 1, 1, true>(a, s);
+        if (p.i8) return p.w1 ? mm_launch<true, false, true, 64, 1, 1, true>(a, s) : mm_launch<true, false, false, 64, 1, 2, true>(a, s);
+        return p.grad ? mm_launch<false, true, false, 64, 1, 2, true>(a, s) : mm_launch<false, false, false, 64, 1, 2, true>(a, s);
     }
-    if (shape == 0) {
-        if (p.i8) return p.w1 ? mm_launch<true, false, true, 16, 1, 1, false>(a, s) : mm_launch<true, false, false, 16, 1, 1, false>(a, s);
-        return p.grad ? mm_launch<false, true, false, 16, 1, 1, false>(a, s) : mm_launch<false, false, false, 16, 1, 1, false>(a, s);
-    }
-    if (shape == 1) {
-        if (p.i8) return p.w1 ? mm_launch<true, false, true, 64, 1, 1, false>(a, s) : mm_launch<true, false, false, 64, 1, 2, false>(a, s);
-        return p.grad ? mm_launch<false, true, false, 64, 1, 2, false>(a, s) : mm_launch<false, false, false, 64, 1, 2, false>(a, s);
-    }
-    if (p.i8) return p.w1 ? mm_launch<true, false, true, 256, 2, 1, false>(a, s) : mm_launch<true, false, false, 256, 2, 2, false>(a, s);
-    return p.grad ? mm_launch<false, true, false, 256, 2, 2, false>(a, s) : mm_launch<false, false, false, 256, 2, 2, false>(a, s);
+    if (p.i8) return p.w1 ? mm_launch<true, false, true, 64, 1, 1, false>(a, s) : mm_launch<true, false, false, 64, 1, 2, false>(a, s);
+    return p.grad ? mm_launch<false, true, false, 64, 1, 2, false>(a, s) : mm_launch<false, false, false, 64, 1, 2, false>(a, s);
 }
 
 }  // namespace moe

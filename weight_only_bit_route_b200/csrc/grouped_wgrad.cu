@@ -25,8 +25,9 @@ namespace moe {
 
 constexpr int WG_THREADS = 384;
 constexpr int WG_EPI_WARPS = 8;
+// NT: input features per tile; CG: CTAs per tile; Z: CTAs that share a tile's rows
 
-template <int NT, int CG>
+template <int NT, int CG, int Z>
 struct WgCfg {
     static constexpr int kBoxesB = NT / CG / 64;                  // 64-feature boxes of x this CTA stages
     static constexpr int kBox = 64 * 128;
@@ -36,6 +37,8 @@ struct WgCfg {
     static constexpr int kHalf = NT / 2;                          // columns of one epilogue warp
     static constexpr int kChunk = 8;                              // K blocks summed in tensor memory at a time
     static constexpr int kTmem = 2 * NT;
+    static_assert(Z == 1 || (CG == 1 && (Z - 1) * (kHalf / Z) * 4 * 32 * WG_EPI_WARPS <= kStages * kStage),
+                  "split rows: the partial sums fit the ring");
     static_assert(kBoxesB % 2 == 0, "one copy brings two boxes");
     static_assert(kTmem <= 512 && kStages >= 3 && kStages <= 16, "tile shape");
 };
@@ -45,14 +48,30 @@ struct WgArgs {
     CUtensorMap d;                       // dw [E][out][in]: boxes of 128 bytes x 32 rows
     const int32_t* offsets;
     int32_t* status;
+    void* dw;
     int E, out_dim, in_dim, rows;
     int f16, out_f32, accumulate;
     int chunked;                         // a and b are the views [1][features / 64][rows][64] (multiples of 64)
 };
 
-template <int NT, int CG>
+// Two fp32 values to 16 bits, low half first
+__device__ __forceinline__ uint32_t wg_pair(float lo, float hi, int f16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return f16 ? *reinterpret_cast<const uint32_t*>(&h) : *reinterpret_cast<const uint32_t*>(&b);
+}
+// All threads of the cluster, each once per step, from wherever its role ends
+__device__ __forceinline__ void wg_cluster_step() {
+    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+}
+template <int W, int Z, int N>
+__device__ __forceinline__ float4 wg_pick(const float (&sum)[N], int r, int j) {      // r and j are constants after unrolling
+    return make_float4(sum[r * W + 4 * j], sum[r * W + 4 * j + 1], sum[r * W + 4 * j + 2], sum[r * W + 4 * j + 3]);
+}
+
+template <int NT, int CG, int Z>
 __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_constant__ WgArgs a) {
-    using C = WgCfg<NT, CG>;
+    using C = WgCfg<NT, CG, Z>;
     constexpr int S = C::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ __align__(8) uint64_t full[S], empty[S], tail[S], acc_full[2], acc_empty[2], drain, hold_bar;
@@ -62,8 +81,10 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = CG == 2 ? g_cta_rank() : 0u;
+    const uint32_t zr = Z > 1 ? g_cta_rank() : 0u;          // this CTA's share of a tile's rows
     const int MT = (a.out_dim + 128 * CG - 1) / (128 * CG), NTN = (a.in_dim + NT - 1) / NT;
 
+    if (warp == 4 && lane < 3) g_prefetch_map(lane == 0 ? &a.a : lane == 1 ? &a.b : &a.d);
     if (tid == 0) {
         for (int s = 0; s < S; s++) {
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(g_smem(&full[s])), "r"(2 * CG));
@@ -82,7 +103,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
     }
     if (warp == 2) g_tmem_alloc<CG>(g_smem(&s_tmem), C::kTmem);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (tid == 0) {
+    if (tid == WG_THREADS - 1) {
         s_ab.limit_ns = g_limit_from(a.status);
         s_hold = g_hold_from(a.status);
     }
@@ -110,11 +131,12 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
     __syncthreads();
     if (CG == 2) g_cluster_sync();
     g_fence_after();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (they wait for this kernel's end themselves)
 
     const uint32_t tmem = s_tmem;
     const int per_e = MT * NTN;
-    const MmSequence seq(int(blockIdx.x) / CG, int(gridDim.x) / CG, a.E * per_e, kSort);
-    struct Tile { int e, base, n, m0, n0; };
+    const MmSequence seq(int(blockIdx.x) / (CG * Z), int(gridDim.x) / (CG * Z), a.E * per_e, kSort);
+    struct Tile { int e, base, n, m0, n0; };                // base, n: the rows this CTA sums
     auto tile_of = [&](int tile) {
         Tile t;
         const int rank = tile / per_e, local = tile - rank * per_e;
@@ -122,6 +144,11 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
         t.e = sp.x;
         t.base = sp.y;
         t.n = sp.z;
+        if (Z > 1) {                                        // whole blocks of 64 rows to each
+            const int per = (t.n + 64 * Z - 1) / (64 * Z) * 64, first = min(int(zr) * per, t.n);
+            t.base += first;
+            t.n = min(per, t.n - first);
+        }
         t.m0 = (local % MT) * (128 * CG);
         t.n0 = (local / MT) * NT;
         return t;
@@ -277,10 +304,10 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
         const uint32_t lane_addr = uint32_t(q * 32) << 16;
         uint8_t* buf = outb + (warp - 4) * 8192;
         int t = 0, nst = 0;
-        bool ok = true;
+        bool ok = true, finished = false;
         for (int i = 0; i < seq.count && ok && !g_aborted(&s_ab); i++) {
             const Tile T = tile_of(seq.tile(i));
-            if (T.n == 0 && a.accumulate) continue;
+            if (Z == 1 && T.n == 0 && a.accumulate) continue;
             const int m0 = T.m0 + int(rank) * 128 + q * 32, x0 = T.n0 + c0;
             float sum[C::kHalf];
 #pragma unroll
@@ -309,6 +336,65 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
                 }
             }
             if (!ok) break;
+            if constexpr (Z > 1) {
+                // (one tile per CTA at most.)  Each CTA of the cluster finishes a Z-th of every warp's columns.
+                constexpr int W = C::kHalf / Z;
+                wg_cluster_step();                          // every CTA's MMAs are done: the rings are free
+#pragma unroll
+                for (int r = 0; r < Z; r++) {
+                    if (r == int(zr)) continue;
+                    const uint32_t to = g_mapa(g_smem(ring), r) +
+                                        ((zr < uint32_t(r) ? zr : zr - 1) * WG_EPI_WARPS + (warp - 4)) * (W * 128) + lane * 16;
+#pragma unroll
+                    for (int j = 0; j < W / 4; j++)
+                        g_st_cluster4(to + j * 512, __float_as_uint(sum[r * W + 4 * j]), __float_as_uint(sum[r * W + 4 * j + 1]),
+                                      __float_as_uint(sum[r * W + 4 * j + 2]), __float_as_uint(sum[r * W + 4 * j + 3]));
+                }
+                wg_cluster_step();
+                float mine[W];
+#pragma unroll
+                for (int j = 0; j < W; j++) mine[j] = 0.f;
+#pragma unroll
+                for (int r = 0; r < Z; r++) {               // in the order of the CTAs
+                    const uint8_t* p = ring + ((zr > uint32_t(r) ? r : r - 1) * WG_EPI_WARPS + (warp - 4)) * (W * 128) + lane * 16;
+#pragma unroll
+                    for (int j = 0; j < W / 4; j++) {
+                        float4 v;
+                        if (r == int(zr)) v = wg_pick<W, Z>(sum, r, j);
+                        else v = *reinterpret_cast<const float4*>(p + j * 512);
+                        mine[4 * j] += v.x;
+                        mine[4 * j + 1] += v.y;
+                        mine[4 * j + 2] += v.z;
+                        mine[4 * j + 3] += v.w;
+                    }
+                }
+                const int row = m0 + lane, x = x0 + int(zr) * W;
+                if (row < a.out_dim) {
+                    const size_t at = (size_t(T.e) * a.out_dim + row) * a.in_dim + x;
+#pragma unroll
+                    for (int j = 0; j < W; j += 8) {        // (in_dim is a multiple of 8)
+                        if (x + j >= a.in_dim) break;
+                        if (a.out_f32) {
+                            float* d = static_cast<float*>(a.dw) + at + j;
+#pragma unroll
+                            for (int i = 0; i < 8; i += 4) {
+                                float4 o = make_float4(mine[j + i], mine[j + i + 1], mine[j + i + 2], mine[j + i + 3]);
+                                if (a.accumulate) {
+                                    const float4 b = *reinterpret_cast<const float4*>(d + i);
+                                    o = make_float4(o.x + b.x, o.y + b.y, o.z + b.z, o.w + b.w);
+                                }
+                                *reinterpret_cast<float4*>(d + i) = o;
+                            }
+                        } else {
+                            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dw) + at + j) =
+                                make_uint4(wg_pair(mine[j], mine[j + 1], a.f16), wg_pair(mine[j + 2], mine[j + 3], a.f16),
+                                           wg_pair(mine[j + 4], mine[j + 5], a.f16), wg_pair(mine[j + 6], mine[j + 7], a.f16));
+                        }
+                    }
+                }
+                finished = true;
+                continue;
+            }
             // 128 bytes of 32 rows at a time; nothing of the tile is stored past the tensor's edge
             auto put = [&](int x, auto piece) {
                 if (m0 >= a.out_dim || x >= a.in_dim) return;
@@ -333,22 +419,27 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
                                           __float_as_uint(sum[c + 4 * i + 2]), __float_as_uint(sum[c + 4 * i + 3]));
                     });
             } else {
-                auto pair = [&](float lo, float hi) {
-                    const __half2 h = __floats2half2_rn(lo, hi);
-                    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-                    return a.f16 ? *reinterpret_cast<const uint32_t*>(&h) : *reinterpret_cast<const uint32_t*>(&b);
-                };
 #pragma unroll
                 for (int c = 0; c < C::kHalf; c += 64)
                     put(x0 + c, [&](int i) {
                         const float* p = sum + c + 8 * i;
-                        return make_uint4(pair(p[0], p[1]), pair(p[2], p[3]), pair(p[4], p[5]), pair(p[6], p[7]));
+                        return make_uint4(wg_pair(p[0], p[1], a.f16), wg_pair(p[2], p[3], a.f16), wg_pair(p[4], p[5], a.f16),
+                                          wg_pair(p[6], p[7], a.f16));
                     });
             }
         }
         if (!ok) fail();
         if (lane == 0) g_store_wait();
         __syncwarp();
+        if (Z > 1 && !finished) {                           // no tile, or an expired wait: the other CTAs still count on it
+            wg_cluster_step();
+            wg_cluster_step();
+        }
+    }
+    if (Z > 1 && warp < 4) {
+        __syncwarp();
+        wg_cluster_step();
+        wg_cluster_step();
     }
 
     g_fence_before();
@@ -398,15 +489,16 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
     }
 }
 
-template <int NT, int CG>
+template <int NT, int CG, int Z>
 static int wg_launch(const WgArgs& a, cudaStream_t s) {
-    using C = WgCfg<NT, CG>;
-    auto k = wgrad_kernel<NT, CG>;
+    using C = WgCfg<NT, CG, Z>;
+    auto k = wgrad_kernel<NT, CG, Z>;
     constexpr int kFixed = C::kStages * C::kStage + C::kOutBytes + 1024;
     int sms = 0;
     const int rc = mm_kernel_ready(reinterpret_cast<const void*>(k), kFixed + 16 * kMaxE, &sms);
     if (rc != MOE_OK) return rc;
-    return mm_launch_cfg(k, dim3(sms / CG * CG), dim3(WG_THREADS), kFixed + 16 * a.E, CG, s, a);
+    const int tiles = a.E * ((a.out_dim + 128 * CG - 1) / (128 * CG)) * ((a.in_dim + NT - 1) / NT);
+    return mm_launch_cfg(k, dim3(Z > 1 ? tiles * Z : sms / CG * CG), dim3(WG_THREADS), kFixed + 16 * a.E, CG * Z, s, a);
 }
 
 int launch_grouped_wgrad(const WgradProblem& p, cudaStream_t s) {
@@ -434,6 +526,7 @@ int launch_grouped_wgrad(const WgradProblem& p, cudaStream_t s) {
     if (int64_t(p.E) * ((p.out_dim + 127) / 128) * ((p.in_dim + 127) / 128) > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
     a.offsets = p.offsets;
     a.status = p.status;
+    a.dw = p.dw;
     a.E = p.E;
     a.out_dim = p.out_dim;
     a.in_dim = p.in_dim;
@@ -444,7 +537,10 @@ int launch_grouped_wgrad(const WgradProblem& p, cudaStream_t s) {
     // Few rows per expert: the tiles are short and the writes bound them, single CTAs keep more of them in flight
     // (4096 x 1536, bf16: 352 experts of 47 rows 849 us against 985 in pairs; 44 of 372 rows 285 against 291; 44 of
     // 1490 rows 852 against 686).
-    return p.rows <= 512 * int64_t(p.E) || a.out_dim <= 128 ? wg_launch<256, 1>(a, s) : wg_launch<256, 2>(a, s);
+    // Few tiles and many rows: clusters of four share a tile's rows.
+    const int64_t tiles = int64_t(p.E) * ((a.out_dim + 127) / 128) * ((a.in_dim + 255) / 256);
+    if (tiles * 4 <= 148 && p.rows >= 512 * int64_t(p.E)) return wg_launch<256, 1, 4>(a, s);
+    return p.rows <= 512 * int64_t(p.E) || a.out_dim <= 128 ? wg_launch<256, 1, 1>(a, s) : wg_launch<256, 2, 1>(a, s);
 }
 
 }  // namespace moe
