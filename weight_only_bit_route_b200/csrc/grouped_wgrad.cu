@@ -16,6 +16,7 @@
 // clips at the tensor's edges.  The tensor core's fp32 sums are cut off rather than rounded, an error that grows with
 // the number of rows; so only 512 rows are summed in tensor memory at a time, and the epilogue adds those partial
 // sums in fp32 registers, rounded to nearest (a 65,536-row batch over 44 experts: 4.4e-6 of the result in one sum).
+#include <algorithm>
 #include <cstring>
 
 #include "grouped_mm.cuh"
@@ -32,15 +33,18 @@ struct WgCfg {
     static constexpr int kBoxesB = NT / CG / 64;                  // 64-feature boxes of x this CTA stages
     static constexpr int kBox = 64 * 128;
     static constexpr int kStage = (2 + kBoxesB) * kBox;
-    static constexpr int kOutBytes = WG_EPI_WARPS * 2 * 4096;     // per epilogue warp: two 32-row x 128-byte buffers
-    static constexpr int kStages = (208 * 1024 - kOutBytes) / kStage;
+    // per epilogue warp: 32-row x 128-byte buffers; a pair's tiles are long, and the room serves the operands better
+    static constexpr int kOutBufs = CG == 2 ? 1 : 2;
+    static constexpr int kOutBytes = WG_EPI_WARPS * kOutBufs * 4096;
+    static constexpr int kMaxStages = 6, kMinStages = (208 * 1024 - kOutBytes) / kStage;      // (with the largest table)
+    static constexpr int kFixed = kOutBytes + 1024;               // beside the stages and 16 bytes per expert
     static constexpr int kHalf = NT / 2;                          // columns of one epilogue warp
     static constexpr int kChunk = 8;                              // K blocks summed in tensor memory at a time
     static constexpr int kTmem = 2 * NT;
-    static_assert(Z == 1 || (CG == 1 && (Z - 1) * (kHalf / Z) * 4 * 32 * WG_EPI_WARPS <= kStages * kStage),
+    static_assert(Z == 1 || (CG == 1 && (Z - 1) * (kHalf / Z) * 4 * 32 * WG_EPI_WARPS <= kMinStages * kStage),
                   "split rows: the partial sums fit the ring");
     static_assert(kBoxesB % 2 == 0, "one copy brings two boxes");
-    static_assert(kTmem <= 512 && kStages >= 3 && kStages <= 16, "tile shape");
+    static_assert(kTmem <= 512 && kMinStages >= 3 && kMinStages <= kMaxStages, "tile shape");
 };
 
 struct WgArgs {
@@ -51,6 +55,7 @@ struct WgArgs {
     void* dw;
     int E, out_dim, in_dim, rows;
     int f16, out_f32, accumulate;
+    int stages;                          // of the ring: as many as shared memory holds
     int chunked;                         // a and b are the views [1][features / 64][rows][64] (multiples of 64)
 };
 
@@ -72,9 +77,10 @@ __device__ __forceinline__ float4 wg_pick(const float (&sum)[N], int r, int j) {
 template <int NT, int CG, int Z>
 __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_constant__ WgArgs a) {
     using C = WgCfg<NT, CG, Z>;
-    constexpr int S = C::kStages;
+    constexpr int SM = C::kMaxStages;
+    const uint32_t S = uint32_t(a.stages);
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ __align__(8) uint64_t full[S], empty[S], tail[S], acc_full[2], acc_empty[2], drain, hold_bar;
+    __shared__ __align__(8) uint64_t full[SM], empty[SM], tail[SM], acc_full[2], acc_empty[2], drain, hold_bar;
     __shared__ uint32_t s_tmem, s_issued[2], s_tail[2], s_tphase[2];      // of the producers of A and of B
     __shared__ int s_hold;
     __shared__ volatile GAbort s_ab;
@@ -86,7 +92,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
 
     if (warp == 4 && lane < 3) g_prefetch_map(lane == 0 ? &a.a : lane == 1 ? &a.b : &a.d);
     if (tid == 0) {
-        for (int s = 0; s < S; s++) {
+        for (int s = 0; s < SM; s++) {
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(g_smem(&full[s])), "r"(2 * CG));
             asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(g_smem(&empty[s])));
             asm volatile("mbarrier.init.shared::cta.b64 [%0], 2;" ::"r"(g_smem(&tail[s])));
@@ -165,15 +171,15 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
         const CUtensorMap* map = isb ? &a.b : &a.a;
         const int boxes = isb ? C::kBoxesB : 2;
         const uint32_t bytes = uint32_t(boxes) * C::kBox;
-        uint32_t it = 0, tails = 0, tphase = 0;       // per stage: last fill was a tail; phase of its tail barrier
+        uint32_t it = 0, s = 0, ph = 0;               // stages issued; the next one and the parity of its round
+        uint32_t tails = 0, tphase = 0;               // per stage: last fill was a tail; phase of its tail barrier
         bool ok = true;
         for (int i = 0; i < seq.count && ok && !g_aborted(&s_ab); i++) {
             const Tile T = tile_of(seq.tile(i));
             const int KB = (T.n + 63) / 64;
             const int x0 = isb ? T.n0 + int(rank) * (NT / CG) : T.m0 + int(rank) * 128;
             for (int kb = 0; kb < KB; kb++, it++) {
-                const int s = it % S;
-                if (it >= uint32_t(S) && !g_wait_w(g_smem(&empty[s]), ((it / S) - 1) & 1, &s_ab, 32)) {
+                if (!g_wait_w(g_smem(&empty[s]), ph ^ 1, &s_ab, 32)) {      // (a new barrier's phase before the first is over)
                     ok = false;
                     break;
                 }
@@ -207,6 +213,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
                     }
                 }
                 __syncwarp();
+                if (++s == S) { s = 0; ph ^= 1; }
             }
         }
         if (!ok) fail();
@@ -216,7 +223,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
             s_tphase[isb] = tphase;
             // the commits' arrivals here have landed before the CTA exits (the copies: see the end of the kernel)
             if (CG == 2 && !isb && !s_ab.flag)
-                for (uint32_t n = it > uint32_t(S) ? it - S : 0; n < it; n++)
+                for (uint32_t n = it > S ? it - S : 0; n < it; n++)
                     if (!g_wait(g_smem(&empty[n % S]), (n / S) & 1, &s_ab)) { fail(); break; }
         }
         __syncwarp();
@@ -224,14 +231,14 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
         // ---------------- MMA issuer (whole warp, one lane issues) ----------------
         if (s_hold && !g_wait_w(g_smem(&hold_bar), 0, &s_ab)) fail();
         const uint32_t idesc = g_idesc(NT, a.f16 != 0, 128 * CG) | G_IDESC_A_MN | G_IDESC_B_MN;
-        uint32_t it = 0;
+        uint32_t s = 0, ph = 0;
         int t = 0;
         bool ok = true;
         for (int i = 0; i < seq.count && ok && !g_aborted(&s_ab); i++) {
             const Tile T = tile_of(seq.tile(i));
             if (T.n == 0) continue;
             const int KB = (T.n + 63) / 64;
-            for (int kb = 0; kb < KB && ok; kb++, it++) {
+            for (int kb = 0; kb < KB && ok; kb++) {
                 const int kc = kb % C::kChunk;
                 const uint32_t d = tmem + (t & 1) * NT;
                 if (kc == 0) {
@@ -241,8 +248,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
                     }
                     g_fence_after();
                 }
-                const int s = it % S;
-                if (!g_wait_w(g_smem(&full[s]), (it / S) & 1, &s_ab)) {
+                if (!g_wait_w(g_smem(&full[s]), ph, &s_ab)) {
                     ok = false;
                     break;
                 }
@@ -260,6 +266,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
                 }
                 __syncwarp();
                 if (last) t++;
+                if (++s == S) { s = 0; ph ^= 1; }
             }
         }
         if (!ok) fail();
@@ -302,7 +309,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
         // ---------------- epilogue ----------------
         const int q = warp & 3, c0 = (warp - 4) / 4 * C::kHalf;      // my lanes and columns
         const uint32_t lane_addr = uint32_t(q * 32) << 16;
-        uint8_t* buf = outb + (warp - 4) * 8192;
+        uint8_t* buf = outb + (warp - 4) * (C::kOutBufs * 4096);
         int t = 0, nst = 0;
         bool ok = true, finished = false;
         for (int i = 0; i < seq.count && ok && !g_aborted(&s_ab); i++) {
@@ -398,8 +405,8 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
             // 128 bytes of 32 rows at a time; nothing of the tile is stored past the tensor's edge
             auto put = [&](int x, auto piece) {
                 if (m0 >= a.out_dim || x >= a.in_dim) return;
-                uint8_t* st = buf + (nst & 1) * 4096;
-                if (lane == 0) g_store_wait_read<1>();              // the buffer's store before last has read it
+                uint8_t* st = buf + (nst % C::kOutBufs) * 4096;
+                if (lane == 0) g_store_wait_read<C::kOutBufs - 1>();   // the buffer's last store has read it
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 8; i++) *reinterpret_cast<uint4*>(st + g_swz(lane, i)) = piece(i);
@@ -449,7 +456,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
     if (tid == 0 && s_ab.flag) {
         const int big = s_issued[1] > s_issued[0];
         const uint32_t hi = s_issued[big], tl = s_tail[big], ph = s_tphase[big];
-        for (uint32_t n = hi > uint32_t(S) ? hi - S : 0; n < hi; n++) {
+        for (uint32_t n = hi > S ? hi - S : 0; n < hi; n++) {
             const uint32_t s = n % S;
             if (!((tl >> s) & 1)) continue;
             if (n >= s_issued[!big]) g_arrive(g_smem(&tail[s]));
@@ -473,7 +480,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
                     tl = i < 2 ? s_tail[i] : g_ld_cluster(g_mapa(g_smem(&s_tail[i & 1]), 1));
                 }
             }
-            for (uint32_t n = hi > uint32_t(S) ? hi - S : 0; n < hi; n++) {
+            for (uint32_t n = hi > S ? hi - S : 0; n < hi; n++) {
                 if ((tl >> (n % S)) & 1) continue;
                 for (int i = 0; i < 2 * CG; i++)
                     if (n >= n_[i]) g_arrive(g_smem(&full[n % S]));
@@ -493,12 +500,17 @@ template <int NT, int CG, int Z>
 static int wg_launch(const WgArgs& a, cudaStream_t s) {
     using C = WgCfg<NT, CG, Z>;
     auto k = wgrad_kernel<NT, CG, Z>;
-    constexpr int kFixed = C::kStages * C::kStage + C::kOutBytes + 1024;
+    // Dynamic shared memory: what a block may have beside the kernel's static 1 KB.
+    constexpr int kRoom = 227 * 1024 - 1024;
+    static_assert(C::kMinStages * C::kStage + C::kFixed + 16 * kMaxE <= kRoom, "the largest table fits");
     int sms = 0;
-    const int rc = mm_kernel_ready(reinterpret_cast<const void*>(k), kFixed + 16 * kMaxE, &sms);
+    const int rc = mm_kernel_ready(reinterpret_cast<const void*>(k), kRoom, &sms);
     if (rc != MOE_OK) return rc;
+    WgArgs args = a;
+    args.stages = std::min(C::kMaxStages, (kRoom - C::kFixed - 16 * a.E) / C::kStage);
+    const int smem = args.stages * C::kStage + C::kFixed + 16 * a.E;
     const int tiles = a.E * ((a.out_dim + 128 * CG - 1) / (128 * CG)) * ((a.in_dim + NT - 1) / NT);
-    return mm_launch_cfg(k, dim3(Z > 1 ? tiles * Z : sms / CG * CG), dim3(WG_THREADS), kFixed + 16 * a.E, CG * Z, s, a);
+    return mm_launch_cfg(k, dim3(Z > 1 ? tiles * Z : sms / CG * CG), dim3(WG_THREADS), smem, CG * Z, s, args);
 }
 
 int launch_grouped_wgrad(const WgradProblem& p, cudaStream_t s) {
