@@ -212,7 +212,7 @@ def codes_of(x):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
-@pytest.mark.parametrize("rows,cols", [(1, 16), (7, 128), (5, 1008), (33, 4096), (3, 20000)])
+@pytest.mark.parametrize("rows,cols", [(1, 16), (7, 128), (5, 1008), (33, 4096), (3, 20000), (2051, 1536), (2048, 2048)])
 def test_quantize_int8_is_exact(rows, cols, dtype):
     dt = TYPES[dtype]
     g = gen(6)

@@ -8,7 +8,7 @@
 // rounds to the same side, and a tie is exact.  The kernel multiplies by 127 / max|x| first (within 2^-16 of
 // the quotient) and divides only where one of eight neighbours lands within 2^-12 of a tie.
 //
-// One block per row, the row's first 4096 elements kept in registers between the two passes.  Bound by the
+// A block (or a warp) per row, the row's first 4096 (2048) elements kept in registers between the two passes.  Bound by the
 // row's bytes: 2 read and 1 written per element.
 #include <mutex>
 
@@ -17,7 +17,8 @@
 namespace moe {
 
 constexpr int Q8_THREADS = 128;
-constexpr int Q8_KEEP = 4;               // 16-byte chunks per thread kept in registers
+// Rows of up to 2048 elements, many of them: a warp per row (16,384 rows of 1536: 27 us with a block per row)
+constexpr int64_t Q8_WARP_ROWS = 2048, Q8_WARP_COLS = 2048;
 
 // max of the 16-bit magnitudes (sign dropped): as unsigned numbers they order like the values, infinity and NaN last
 __device__ __forceinline__ uint32_t q8_max2(uint32_t m, uint32_t v) { return __vmaxu2(m, v & 0x7fff7fffu); }
@@ -41,47 +42,51 @@ __device__ __forceinline__ long long q8_source(int slot, int top_k, long long ns
     return slot >= 0 && t < nsrc ? t : -1;
 }
 
-template <bool F16>
+template <bool F16, int TPR>           // TPR threads per row: 32 or the block
 __global__ void __launch_bounds__(Q8_THREADS) quant_int8_kernel(const uint16_t* __restrict__ x, long long cols,
                                                                const int32_t* __restrict__ row_slot, int top_k,
                                                                long long nsrc, const int32_t* __restrict__ nrows,
                                                                int8_t* __restrict__ codes, float* __restrict__ scales,
-                                                               int32_t* status) {
+                                                               int32_t* status, long long rows) {
+    constexpr int kKeep = TPR == 32 ? 8 : 4;                          // 16-byte chunks per thread kept in registers
+    const int tid = int(threadIdx.x) % TPR;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the product's weights need nothing from here
-    const long long row = blockIdx.x;
-    if (nrows && row >= *nrows) return;                               // behind the last expert's rows
+    const long long row = (long long)blockIdx.x * (Q8_THREADS / TPR) + threadIdx.x / TPR;
+    if (row >= rows || (nrows && row >= *nrows)) return;                               // behind the last expert's rows
     const long long n = cols / 8;
     uint2* dst = reinterpret_cast<uint2*>(codes + row * cols);
     const long long src = row_slot ? q8_source(row_slot[row], top_k, nsrc) : row;
     if (src < 0) {                                                    // a slot out of range: a zero row
-        if (threadIdx.x == 0) {
+        if (tid == 0) {
             scales[row] = 0.f;
             if (status) set_status(status, MOE_ERR_DEVICE_INDEX);
         }
-        for (long long i = threadIdx.x; i < n; i += Q8_THREADS) dst[i] = make_uint2(0, 0);
+        for (long long i = tid; i < n; i += TPR) dst[i] = make_uint2(0, 0);
         return;
     }
     const uint4* p = reinterpret_cast<const uint4*>(x + src * cols);
-    uint4 keep[Q8_KEEP];
+    uint4 keep[kKeep];
     uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < Q8_KEEP; j++) {
-        const long long i = threadIdx.x + j * Q8_THREADS;
+    for (int j = 0; j < kKeep; j++) {
+        const long long i = tid + j * TPR;
         keep[j] = i < n ? p[i] : make_uint4(0, 0, 0, 0);
         m = q8_max8(m, keep[j]);
     }
-    for (long long i = threadIdx.x + Q8_KEEP * Q8_THREADS; i < n; i += Q8_THREADS) m = q8_max8(m, p[i]);
+    for (long long i = tid + kKeep * TPR; i < n; i += TPR) m = q8_max8(m, p[i]);
     for (int o = 16; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-    __shared__ uint32_t sm[Q8_THREADS / 32];
-    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = m;
-    __syncthreads();
+    if constexpr (TPR > 32) {
+        __shared__ uint32_t sm[TPR / 32];
+        if ((tid & 31) == 0) sm[tid >> 5] = m;
+        __syncthreads();
 #pragma unroll
-    for (int w = 0; w < Q8_THREADS / 32; w++) m = __vmaxu2(m, sm[w]);
+        for (int w = 0; w < TPR / 32; w++) m = __vmaxu2(m, sm[w]);
+    }
     m = max(m & 0xffffu, m >> 16);
     const bool bad = m >= (F16 ? 0x7c00u : 0x7f80u);
     const float amax = act_lo<F16>(m);
-    if (threadIdx.x == 0) {
+    if (tid == 0) {
         scales[row] = bad ? __int_as_float(0x7fffffff) : __fdiv_rn(amax, 127.f);
         if (bad && status) set_status(status, MOE_ERR_NONFINITE);
     }
@@ -109,20 +114,23 @@ __global__ void __launch_bounds__(Q8_THREADS) quant_int8_kernel(const uint16_t* 
         dst[i] = o;
     };
 #pragma unroll
-    for (int j = 0; j < Q8_KEEP; j++) {
-        const long long i = threadIdx.x + j * Q8_THREADS;
+    for (int j = 0; j < kKeep; j++) {
+        const long long i = tid + j * TPR;
         if (i < n) put(i, keep[j]);
     }
-    for (long long i = threadIdx.x + Q8_KEEP * Q8_THREADS; i < n; i += Q8_THREADS) put(i, p[i]);
+    for (long long i = tid + kKeep * TPR; i < n; i += TPR) put(i, p[i]);
 }
 
 int launch_quant_int8(const void* x, bool f16, int64_t rows, int64_t cols, const int32_t* row_slot, int top_k,
                       int64_t nsrc, const int32_t* nrows, int8_t* codes, float* scales, int32_t* status,
                       cudaStream_t s) {
     if (rows <= 0) return MOE_OK;
-    auto k = f16 ? quant_int8_kernel<true> : quant_int8_kernel<false>;
-    return mm_launch_cfg(k, dim3(unsigned(rows)), dim3(Q8_THREADS), 0, 1, s, static_cast<const uint16_t*>(x),
-                         (long long)cols, row_slot, top_k, (long long)nsrc, nrows, codes, scales, status);
+    const bool warp = rows >= Q8_WARP_ROWS && cols <= Q8_WARP_COLS;
+    auto k = warp ? (f16 ? quant_int8_kernel<true, 32> : quant_int8_kernel<false, 32>)
+                  : (f16 ? quant_int8_kernel<true, Q8_THREADS> : quant_int8_kernel<false, Q8_THREADS>);
+    const int64_t blocks = warp ? (rows + Q8_THREADS / 32 - 1) / (Q8_THREADS / 32) : rows;
+    return mm_launch_cfg(k, dim3(unsigned(blocks)), dim3(Q8_THREADS), 0, 1, s, static_cast<const uint16_t*>(x),
+                         (long long)cols, row_slot, top_k, (long long)nsrc, nrows, codes, scales, status, (long long)rows);
 }
 
 // One block per row, 16 bytes per thread and step.
