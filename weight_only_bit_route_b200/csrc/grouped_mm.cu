@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
             const int r0 = T.n0 + int(rank) * half, m0 = T.m0 + int(rank) * 128;
             for (int ks = ks0; ks < ks1; ks++, it++) {
                 const int s = it % S;
-                if (it >= uint32_t(S) && !g_wait_w(g_smem(&empty[s]), ((it / S) - 1) & 1, &s_ab, 32)) {
+                if (it >= uint32_t(S) && !g_wait_long(g_smem(&empty[s]), ((it / S) - 1) & 1, &s_ab)) {
                     ok = false;
                     break;
                 }
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
     } else if (warp == 1 && rank == 0) {
         // ---------------- MMA issuer (whole warp, one lane issues) ----------------
         // failure testing (moe_set_wait_hold): wait for a barrier that nothing completes
-        if (s_hold && !g_wait_w(g_smem(&hold_bar), 0, &s_ab)) fail();
+        if (s_hold && !g_wait_long(g_smem(&hold_bar), 0, &s_ab)) fail();
         uint32_t it = 0;
         MmHalves acc;
         bool ok = true;
@@ -359,8 +359,8 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
             const uint32_t d = tmem + h * C::kHalfCols, up = both ? NT : C::kHalfRows;
             const int half = T.bn / CG;
             const uint32_t slice = (half <= 16 ? 16u : half <= 32 ? 32u : half <= 64 ? 64u : 128u) * 128u;
-            if ((acc.uses(h) && !g_wait_w(g_smem(&acc_empty[h]), (acc.uses(h) - 1) & 1, &s_ab)) ||
-                (both && acc.u1 && !g_wait_w(g_smem(&acc_empty[1]), (acc.u1 - 1) & 1, &s_ab))) {
+            if ((acc.uses(h) && !g_wait_long(g_smem(&acc_empty[h]), (acc.uses(h) - 1) & 1, &s_ab)) ||
+                (both && acc.u1 && !g_wait_long(g_smem(&acc_empty[1]), (acc.u1 - 1) & 1, &s_ab))) {
                 ok = false;
                 break;
             }
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
             g_fence_after();
             for (int ks = ks0; ks < ks1; ks++, it++) {
                 const int s = it % S;
-                if (!g_wait_w(g_smem(&full[s]), (it / S) & 1, &s_ab)) {
+                if (!g_wait_long(g_smem(&full[s]), (it / S) & 1, &s_ab)) {
                     ok = false;
                     break;
                 }
@@ -445,8 +445,8 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
             }
             const bool both = T.bn > C::kHalfRows;
             const uint32_t h = both ? 0 : use.next;
-            if (!g_wait_w(g_smem(&acc_full[h]), use.uses(h) & 1, &s_ab, 32) ||
-                (both && !g_wait_w(g_smem(&acc_full[1]), use.u1 & 1, &s_ab, 32))) {
+            if (!g_wait_long(g_smem(&acc_full[h]), use.uses(h) & 1, &s_ab) ||
+                (both && !g_wait_long(g_smem(&acc_full[1]), use.u1 & 1, &s_ab))) {
                 ok = false;
                 break;
             }
@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
             uint16_t* dst = a.out + size_t(T.n0 + odd) * a.mdim + (m - odd);
             if constexpr (SPLIT) {
                 // Block b of 16 rows is summed by CTA b mod z: hand it the others' partial sums, then wait for theirs.
-                if (ti > 0 && !g_wait_w(g_smem(&red_free), (ti - 1) & 1, &s_ab, 32)) {
+                if (ti > 0 && !g_wait_long(g_smem(&red_free), (ti - 1) & 1, &s_ab)) {
                     ok = false;
                     break;
                 }
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
                 g_fence_cluster();
                 __syncwarp();
                 if (lane < z && lane != int(krank)) g_arrive_remote(g_mapa(g_smem(&red_full), lane));
-                if (!g_wait_w(g_smem(&red_full), ti & 1, &s_ab, 32)) {
+                if (!g_wait_long(g_smem(&red_full), ti & 1, &s_ab)) {
                     ok = false;
                     break;
                 }

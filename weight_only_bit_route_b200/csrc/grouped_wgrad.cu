@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
             const int KB = (T.n + 63) / 64;
             const int x0 = isb ? T.n0 + int(rank) * (NT / CG) : T.m0 + int(rank) * 128;
             for (int kb = 0; kb < KB; kb++, it++) {
-                if (!g_wait_w(g_smem(&empty[s]), ph ^ 1, &s_ab, 32)) {      // (a new barrier's phase before the first is over)
+                if (!g_wait_long(g_smem(&empty[s]), ph ^ 1, &s_ab)) {      // (a new barrier's phase before the first is over)
                     ok = false;
                     break;
                 }
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
         __syncwarp();
     } else if (warp == 1 && rank == 0) {
         // ---------------- MMA issuer (whole warp, one lane issues) ----------------
-        if (s_hold && !g_wait_w(g_smem(&hold_bar), 0, &s_ab)) fail();
+        if (s_hold && !g_wait_long(g_smem(&hold_bar), 0, &s_ab)) fail();
         const uint32_t idesc = g_idesc(NT, a.f16 != 0, 128 * CG) | G_IDESC_A_MN | G_IDESC_B_MN;
         uint32_t s = 0, ph = 0;
         int t = 0;
@@ -242,13 +242,13 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
                 const int kc = kb % C::kChunk;
                 const uint32_t d = tmem + (t & 1) * NT;
                 if (kc == 0) {
-                    if (t >= 2 && !g_wait_w(g_smem(&acc_empty[t & 1]), ((t >> 1) - 1) & 1, &s_ab)) {
+                    if (t >= 2 && !g_wait_long(g_smem(&acc_empty[t & 1]), ((t >> 1) - 1) & 1, &s_ab)) {
                         ok = false;
                         break;
                     }
                     g_fence_after();
                 }
-                if (!g_wait_w(g_smem(&full[s]), ph, &s_ab)) {
+                if (!g_wait_long(g_smem(&full[s]), ph, &s_ab)) {
                     ok = false;
                     break;
                 }
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
             it += KB;
             if (!(T.n & 15)) continue;
             const uint32_t s = (it - 1) % S;
-            if (!g_wait_w(g_smem(&tail[s]), (tphase >> s) & 1, &s_ab, 32)) {
+            if (!g_wait_long(g_smem(&tail[s]), (tphase >> s) & 1, &s_ab)) {
                 ok = false;
                 break;
             }
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
             for (int i = 0; i < C::kHalf; i++) sum[i] = 0.f;
             const int chunks = ((T.n + 63) / 64 + C::kChunk - 1) / C::kChunk;
             for (int ch = 0; ch < chunks; ch++, t++) {
-                if (!g_wait_w(g_smem(&acc_full[t & 1]), (t >> 1) & 1, &s_ab, 32)) {
+                if (!g_wait_long(g_smem(&acc_full[t & 1]), (t >> 1) & 1, &s_ab)) {
                     ok = false;
                     break;
                 }

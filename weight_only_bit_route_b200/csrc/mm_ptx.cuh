@@ -6,6 +6,23 @@
 
 namespace moe {
 
+// Bounded warp-wide wait (as g_wait_w) that lets the hardware suspend the warp for up to 10 us a try instead of polling:
+// the waiting roles then cost no power, which is what bounds long batches.
+__device__ __forceinline__ bool g_try_long(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok) : "r"(bar), "r"(parity), "r"(10000u) : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool g_wait_long(uint32_t bar, uint32_t parity, volatile GAbort* ab) {
+    if (__all_sync(0xffffffffu, g_try_long(bar, parity))) return true;
+    const unsigned long long t0 = g_timer();
+    while (true) {
+        if (__all_sync(0xffffffffu, g_try_long(bar, parity))) return true;
+        if (__any_sync(0xffffffffu, ab->flag || g_timer() - t0 > ab->limit_ns)) return false;
+    }
+}
+
 __device__ __forceinline__ void g_tma3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
