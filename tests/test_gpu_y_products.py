@@ -141,6 +141,46 @@ def test_an_expert_keeps_its_infinities():
     assert torch.equal(got[2][0], clean[2][0]) and torch.equal(got[2][2], clean[2][2])
 
 
+def test_most_experts():
+    """1024 experts, few and many rows: the whole table, and its order by size."""
+    E, K, N = 1024, 72, 136
+    g = gen(21)
+    for rows_per in (1, 70):
+        counts = torch.randint(0, 2 * rows_per + 1, (E,), generator=g, device="cuda").tolist()
+        counts[3] = 40 * rows_per
+        rows = sum(counts)
+        x, dy, w = normal(g, rows, K), normal(g, rows, N), normal(g, E, N, K, std=0.1)
+        off, ws = offsets_of(counts), moe.control_block()
+        y, dx = moe.grouped_mm(x, w, off, ws), moe.grouped_mm_dgrad(dy, w, off, ws)
+        dw = moe.grouped_mm_wgrad(dy, x, off, ws, out_dtype=torch.float32)
+        assert moe.read_status(ws) == 0
+        for e, a, b in spans(counts):
+            xe, de, we = x[a:b].double(), dy[a:b].double(), w[e].double()
+            for got, p, q, terms in ((y[a:b], xe, we.T, K), (dx[a:b], de, we, N), (dw[e], de.T, xe, b - a)):
+                ref = p @ q
+                assert ((got.double() - ref).abs() <= product_bound(p.abs() @ q.abs(), terms, ref, got.dtype)).all(), e
+
+
+def test_offsets_past_32_bits():
+    """Outputs of more than 2^31 elements: the last rows (and the last expert's gradient) are where they belong."""
+    K, N, rows, E = 64, 4096, 560_000, 3
+    g = gen(22)
+    x, w = normal(g, rows, K), normal(g, E, N, K, std=0.1)
+    off, ws = offsets_of([200_000, 0, 360_000]), moe.control_block()
+    y = moe.grouped_mm(x, w, off, ws)
+    assert y.numel() > 2 ** 31
+    for a, e in ((0, 0), (199_990, 0), (200_000, 2), (530_000, 2), (rows - 10, 2)):
+        xe, we = x[a:a + 10].double(), w[e].double()
+        ref = xe @ we.T
+        assert ((y[a:a + 10].double() - ref).abs() <= product_bound(xe.abs() @ we.abs().T, K, ref, y.dtype)).all(), a
+    dx = moe.grouped_mm_dgrad(y, w, off, ws)                   # an input of more than 2^31 elements
+    for a, e in ((0, 0), (rows - 10, 2)):
+        ye, we = y[a:a + 10].double(), w[e].double()
+        ref = ye @ we
+        assert ((dx[a:a + 10].double() - ref).abs() <= product_bound(ye.abs() @ we.abs(), N, ref, dx.dtype)).all(), a
+    assert moe.read_status(ws) == 0
+
+
 def test_products_repeat_bit_for_bit():
     counts = [300, 0, 77, 1, 512]
     g = gen(3)
@@ -333,6 +373,58 @@ def test_int8_largest_sums():
     assert ((y.double() - v).abs() <= v.abs() * (2.0 ** -8 + 2.0 ** -20)).all()
 
 
+def test_int8_slots_out_of_range_and_repeated():
+    """row_slot as a caller may make it: the same token for several rows is fine; a slot outside the batch gives a
+    zero row and is reported."""
+    counts, k, H, F = [12, 20], 8, 256, 128
+    g = gen(23)
+    x = normal(g, 4, H)
+    gate, up, down = int8_bank(g, 2, F, H), int8_bank(g, 2, F, H), int8_bank(g, 2, H, F)
+    off, ws = offsets_of(counts), moe.workspace(4, H, 2, F, 2)
+    same = torch.full((32,), 17, dtype=torch.int32, device="cuda")                 # token 2, every row
+    h = moe.grouped_swiglu(x, off, same, k, gate, up, 32, ws)
+    assert moe.read_status(ws) == 0
+    assert torch.equal(h[:12], h[:1].expand(12, F)) and torch.equal(h[12:], h[12:13].expand(20, F))
+    rs = routing(counts, k, g)
+    ref = moe.grouped_swiglu(x, off, rs, k, gate, up, 32, ws)
+    for bad in (-1, 32, 2 ** 31 - 1, -2 ** 31):
+        r = rs.clone()
+        r[5] = bad
+        h = moe.grouped_swiglu(x, off, r, k, gate, up, 32, ws)
+        assert moe.read_status(ws) == ERR_INDEX
+        keep = torch.arange(32, device="cuda") != 5
+        assert (h[5] == 0).all() and torch.equal(h[keep], ref[keep])
+        tw = torch.ones(32, device="cuda")
+        y = moe.grouped_down(ref, off, r, tw, down, ws)
+        assert moe.read_status(ws) == ERR_INDEX and (y[5] == 0).all()
+
+
+def test_int8_many_tokens_take_the_copy():
+    """A batch large enough that tokens are quantised once and their codes copied gives the bits of the small one."""
+    T, k, E, H, F = 1100, 8, 8, 2048, 128
+    g = gen(24)
+    x = normal(g, T, H)
+    gate, up = int8_bank(g, E, F, H), int8_bank(g, E, F, H)
+    ids = torch.rand(T, E, generator=g, device="cuda").argsort(1).to(torch.int32).contiguous()
+    ws = moe.workspace(T, H, E, F, k)
+    off, rs, sr = moe.permute(ids, E, ws)
+    h = moe.grouped_swiglu(x, off, rs, k, gate, up, T * k, ws)
+    assert moe.read_status(ws) == 0
+    qx, sx = codes_of(x)
+    o = off.tolist()
+    for e in range(E):
+        tok = (rs[o[e]:o[e + 1]] // k).long()
+        gg, uu = product8(qx[tok], sx[tok], gate, e), product8(qx[tok], sx[tok], up, e)
+        ref = gg * torch.sigmoid(gg) * uu
+        bound = ref.abs() * (2.0 ** -8 + (1 + gg.abs()) * 2.0 ** -20) + 1e-30
+        assert ((h[o[e]:o[e + 1]].double() - ref).abs() <= bound).all(), e
+    x[7, 3] = float("inf")                         # seen by the token pass, carried by the copy
+    h2 = moe.grouped_swiglu(x, off, rs, k, gate, up, T * k, ws)
+    assert moe.read_status(ws) == ERR_NONFINITE
+    bad = (rs // k) == 7
+    assert h2[bad].isnan().all() and torch.equal(h2[~bad], h[~bad])
+
+
 def test_int8_nonfinite_row_is_reported():
     counts, k, H, F = [8, 0, 24], 8, 256, 128
     g = gen(10)
@@ -513,6 +605,7 @@ def _large_calls():
     rows = sum(counts)
     x, dy, w = normal(g, rows, 520), normal(g, rows, 392), normal(g, 4, 392, 520)
     xs, ws_ = normal(g, 63, 2048), normal(g, 2, 136, 2048)
+    xl, dyl, offl = normal(g, 601, 1024), normal(g, 601, 1536), offsets_of([601])
     off, offs, rs = offsets_of(counts), offsets_of(few), routing(counts, k, g)
     x8 = normal(g, rows // k, H)
     gate, up, down = int8_bank(g, 4, F, H), int8_bank(g, 4, F, H), int8_bank(g, 4, H, F)
@@ -521,6 +614,7 @@ def _large_calls():
         h = moe.grouped_swiglu(x8, off, rs, k, gate, up, rows, ws)
         return [moe.grouped_mm(x, w, off, ws), moe.grouped_mm_dgrad(dy, w, off, ws), moe.grouped_mm_wgrad(dy, x, off, ws),
                 moe.grouped_mm_wgrad(dy, x, off, ws, out_dtype=torch.float32), moe.grouped_mm(xs, ws_, offs, ws), h,
+                moe.grouped_mm_wgrad(dyl, xl, offl, ws), moe.grouped_mm_wgrad(dyl[:, :136].contiguous(), xl, offl, ws),
                 moe.grouped_down(h, off, rs, None, down, ws)]
 
     return run, lambda: moe.workspace(rows // k, H, 4, F, 4)
@@ -553,7 +647,11 @@ def test_binding_checks_shapes_and_types():
            lambda: moe.grouped_mm(x, w.half(), off, ws), lambda: moe.grouped_mm(x, w, off.cpu(), ws),
            lambda: moe.grouped_mm(x, w, off, ws, out=dy.float()), lambda: moe.grouped_mm_dgrad(x, w, off, ws),
            lambda: moe.grouped_mm_wgrad(dy[:4], x, off, ws), lambda: moe.grouped_mm_wgrad(dy, x, off, ws, accumulate=True),
-           lambda: moe.grouped_mm_wgrad(dy, x, off, ws, out_dtype=torch.float16)]
+           lambda: moe.grouped_mm_wgrad(dy, x, off, ws, out_dtype=torch.float16),
+           lambda: moe.grouped_mm(x, w, off[:2], ws), lambda: moe.grouped_mm(x, w, off, ws.float()),
+           lambda: moe.Bank(moe.FMT_INT8, w, dy), lambda: moe.Bank(moe.FMT_INT8, w.to(torch.int8), None),
+           lambda: moe.Bank(moe.FMT_INT8, w.to(torch.int8), torch.ones(2, 31, device="cuda")),
+           lambda: moe.Bank(moe.FMT_INT8, w.to(torch.int8), torch.ones(2, 32, dtype=torch.bfloat16, device="cuda"))]
     for i, call in enumerate(bad):
         with pytest.raises(moe.MoEError) as err:
             call()

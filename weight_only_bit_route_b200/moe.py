@@ -113,6 +113,17 @@ def _stream():
     return _raw_stream(torch.cuda.current_device())
 
 
+def _on(dev, fn, call, *args):
+    """The call with the tensors' device current, on its current stream."""
+    if torch.cuda.current_device() == dev:
+        code = call(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            code = call(*args, _raw_stream(dev))
+    if code != 0:
+        raise MoEError(fn, code)
+
+
 class Bank:
     """A projection bank in the fused layout [E, out, in] (device tensors).
 
@@ -123,6 +134,11 @@ class Bank:
     """
 
     def __init__(self, fmt, packed, scales=None, global_scale=None, out_dim=None, in_dim=None, input_scale=None):
+        if fmt == FMT_INT8 and not (packed.dtype is torch.int8 and packed.dim() == 3 and packed.is_contiguous()
+                                    and scales is not None and scales.dtype is torch.float32
+                                    and tuple(scales.shape) == tuple(packed.shape[:2]) and scales.is_contiguous()
+                                    and scales.device == packed.device):
+            raise MoEError("int8 bank: packed int8 [E,out,in] and scales fp32 [E,out], contiguous, on one device", -1)
         self.fmt, self.packed, self.scales, self.global_scale = fmt, packed, scales, global_scale
         self.input_scale = input_scale       # NVFP4 W4A4: activation global scale by expert, fp32 [E]
         self.E = packed.shape[0]
@@ -235,10 +251,8 @@ def grouped_swiglu(x, offsets, row_slot, top_k, gate, up, rows, ws, out=None):
     T, H = x.shape
     h = out if out is not None else x.new_empty((rows, gate.out_dim), dtype=torch.bfloat16)
     g, u = gate.struct(), up.struct()
-    _check("moe_grouped_w4a16_swiglu",
-           lib.moe_grouped_w4a16_swiglu(_ptr(x), T, H, _ptr(offsets), _ptr(row_slot), top_k,
-                                        ctypes.byref(g), ctypes.byref(u), 0.0, _ptr(h),
-                                        _ptr(ws), ws.numel(), _stream()))
+    _on(x.get_device(), "moe_grouped_w4a16_swiglu", lib.moe_grouped_w4a16_swiglu, _ptr(x), T, H, _ptr(offsets),
+        _ptr(row_slot), top_k, ctypes.byref(g), ctypes.byref(u), 0.0, _ptr(h), _ptr(ws), ws.numel())
     return h
 
 
@@ -246,9 +260,8 @@ def grouped_down(h_perm, offsets, row_slot, topk_w, down, ws, out=None):
     rows = h_perm.shape[0]
     y = out if out is not None else h_perm.new_empty((rows, down.out_dim), dtype=torch.bfloat16)
     d = down.struct()
-    _check("moe_grouped_w4a16_down",
-           lib.moe_grouped_w4a16_down(_ptr(h_perm), _ptr(offsets), _ptr(row_slot), _ptr(topk_w), rows,
-                                      ctypes.byref(d), _ptr(y), _ptr(ws), ws.numel(), _stream()))
+    _on(h_perm.get_device(), "moe_grouped_w4a16_down", lib.moe_grouped_w4a16_down, _ptr(h_perm), _ptr(offsets),
+        _ptr(row_slot), _ptr(topk_w), rows, ctypes.byref(d), _ptr(y), _ptr(ws), ws.numel())
     return y
 
 
@@ -270,17 +283,6 @@ def _mm_out(fn, out, shape, dtype, like):
     if not (tuple(out.shape) == shape and out.dtype is dtype and out.device == like.device and out.is_contiguous()):
         raise MoEError(f"{fn}: out must be contiguous {dtype} {shape} on the tensors' device", -1)
     return out
-
-
-def _on(dev, fn, call, *args):
-    """The call with the tensors' device current, on its current stream."""
-    if torch.cuda.current_device() == dev:
-        code = call(*args, _raw_stream(dev))
-    else:
-        with torch.cuda.device(dev):
-            code = call(*args, _raw_stream(dev))
-    if code != 0:
-        raise MoEError(fn, code)
 
 
 def grouped_mm(x, w, offsets, ws, out=None):
