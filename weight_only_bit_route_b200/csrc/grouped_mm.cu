@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
         asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(g_smem(&drain)));
         asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(g_smem(&hold_bar)));
         if (SPLIT) {
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(g_smem(&red_full)), "r"((z - 1) * MM_EPI_WARPS));
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(g_smem(&red_full)));
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(g_smem(&red_free)), "r"((z - 1) * MM_EPI_WARPS));
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -172,6 +172,10 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
         s_issued[0] = s_issued[1] = 0;
     }
     if (warp == 2) g_tmem_alloc<CG>(g_smem(&s_tmem), C::kTmem);
+    if (CG == 2 || SPLIT) {                          // the other CTAs' barriers exist before anything arrives there
+        __syncthreads();
+        g_cluster_sync();
+    }
     if (!a.early) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (tid == MM_THREADS - 1) {                     // (a thread with few offsets or none to wait for)
         s_ab.limit_ns = g_limit_from(a.status);
@@ -227,7 +231,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
         if (lane == 31) { s_wsum[warp] = v; s_wt[warp] = w; }
         __syncthreads();
         int base = 0, tbase = 0, tot = 0, ttot = 0;
-        for (int q = 0; q < MM_THREADS / 32; q++) {
+        for (int q = 0; q * 32 * PER < a.E; q++) {                   // (the warps that hold experts)
             if (q < warp) { base += s_wsum[q]; tbase += s_wt[q]; }
             tot += s_wsum[q];
             ttot += s_wt[q];
@@ -240,7 +244,6 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
     }
     g_fence_before();
     __syncthreads();
-    if (CG == 2 || SPLIT) g_cluster_sync();          // the other CTAs' barriers exist before anything arrives there
     g_fence_after();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (they wait for this kernel's end themselves)
 
@@ -459,30 +462,30 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
                     ok = false;
                     break;
                 }
-                for (int b = hsel; b * 16 < T.nval; b += 2) {
+                const int nblk = (T.nval + 15) / 16, nown = (nblk - int(krank) + z - 1) / z;      // blocks; mine of them
+                constexpr uint32_t kPart = C::kMat * 8192;                                        // a block's partial sums
+                const uint32_t per = uint32_t(C::kBlocks / z + (C::kBlocks < z)) * kPart;         // room for one CTA's
+                if (warp == 4 && lane == 0) g_expect(g_smem(&red_full), uint32_t(nown * (z - 1)) * kPart);
+                for (int b = hsel; b < nblk; b += 2) {
                     const uint32_t own = uint32_t(b) & (z - 1);
                     if (own == krank) continue;
-                    const uint32_t slot = krank < own ? krank : krank - 1;
-                    const uint32_t to = g_mapa(g_smem(red), own) + ((slot * (C::kBlocks / z + (C::kBlocks < z)) + uint32_t(b) / z) * C::kMat) * 8192 +
-                                        uint32_t(q * 32 + lane) * 16;
+                    const uint32_t to = g_mapa(g_smem(red), own) + (krank < own ? krank : krank - 1) * per +
+                                        uint32_t(b / z) * kPart + uint32_t(q * 32 + lane) * 16;
+                    const uint32_t bar = g_mapa(g_smem(&red_full), own);
+                    uint32_t v[16], u[16];
+                    g_ld16(acc + b * 16, v);
+                    if constexpr (GU) g_ld16(acc + up + b * 16, u);
+                    g_ld_wait();
 #pragma unroll
-                    for (int mat = 0; mat < C::kMat; mat++) {
-                        uint32_t v[16];
-                        g_ld16(acc + mat * up + b * 16, v);
-                        g_ld_wait();
-#pragma unroll
-                        for (int j = 0; j < 4; j++)
-                            g_st_cluster4(to + mat * 8192 + j * 2048, v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    for (int j = 0; j < 4; j++) {
+                        g_st_async4(to + j * 2048, v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3], bar);
+                        if constexpr (GU) g_st_async4(to + 8192 + j * 2048, u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3], bar);
                     }
                 }
-                g_fence_cluster();
-                __syncwarp();
-                if (lane < z && lane != int(krank)) g_arrive_remote(g_mapa(g_smem(&red_full), lane));
                 if (!g_wait_long(g_smem(&red_full), ti & 1, &s_ab)) {
                     ok = false;
                     break;
                 }
-                g_fence_cluster();
             }
 #pragma unroll
             for (int i = 0; i < (NT + 31) / 32; i++) {
@@ -546,7 +549,14 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
 
     g_fence_before();
     __syncthreads();
-    if (CG == 2 || SPLIT) g_cluster_sync();
+    if (CG == 2) g_cluster_sync();
+    if (SPLIT) {
+        // A CTA that has seen all its partial sums has nothing more coming in; after an expired wait some may still
+        // be on their way (and the barrier that counts them may never complete): let them land.
+        g_cluster_sync_relaxed();
+        if (tid == 0 && s_ab.flag)
+            for (const unsigned long long t0 = g_timer(); g_timer() - t0 < 1000000ull;) __nanosleep(1000);
+    }
     // after an expired wait, copies may be in flight for a stage that only some producers had issued: stand in for
     // the others' arrivals, then wait (bounded) for the last stages
     if (rank == 0 && tid == 0 && (CG == 2 || s_ab.flag)) {

@@ -78,7 +78,11 @@ __device__ __forceinline__ void g_expect_remote(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void g_st_cluster4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
-__device__ __forceinline__ void g_fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+// 16 bytes into another CTA's shared memory, counted there on barrier bar: no fence on either side
+__device__ __forceinline__ void g_st_async4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];"
+                 ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar) : "memory");
+}
 __device__ __forceinline__ void g_prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
@@ -90,6 +94,10 @@ __device__ __forceinline__ uint32_t g_ld_cluster(uint32_t addr) {
 // All threads of the cluster's CTAs (each CTA's threads converged)
 __device__ __forceinline__ void g_cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The same without ordering memory (a release would wait for the CTA's global stores): keeps the CTAs alive together
+__device__ __forceinline__ void g_cluster_sync_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
 }
 // Operand stored along M (or N): 64-element rows of 128 bytes, one row per K, 128-byte swizzle.  8-row groups
 // of K are 1024 bytes apart (stride offset); the next 64 elements along M (or N) follow at lbo bytes.
