@@ -320,7 +320,8 @@ int moe_grouped_w4a16_down(const void* h_perm, const int32_t* expert_offsets,
  * of 8, E <= 1024, tensors 16-byte aligned and contiguous; rows is the row count
  * of the tensors.  Offsets that decrease or leave [0, rows] are clipped to it
  * and recorded as MOE_ERR_DEVICE_INDEX.  Results do not depend on the order in
- * which tiles run.  ws: at least 1024 bytes (the control block), zero-filled
+ * which tiles run; accumulate takes magnitudes below 2^-126 for zero.  Outputs
+ * must not overlap inputs.  ws: at least 1024 bytes (the control block), zero-filled
  * once; it holds no intermediate results. */
 int moe_grouped_mm(const void* x, const int32_t* expert_offsets, int rows, const void* w, int E,
                    int out_dim, int in_dim, int f16, void* y, void* ws, size_t ws_bytes,

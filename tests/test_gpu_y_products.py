@@ -125,6 +125,20 @@ def test_few_tiles_share_a_long_contraction(counts, K, N):
         assert torch.equal(moe.grouped_mm(x, w, off, ws)[:sum(counts)], y[:sum(counts)])
 
 
+def test_no_rows_at_all():
+    """Empty row tensors: nothing to multiply, a zero gradient, an accumulated one left as it was."""
+    off, ws, K, N = offsets_of([0, 0]), moe.control_block(), 72, 136
+    x, dy = torch.empty(0, K, dtype=torch.bfloat16, device="cuda"), torch.empty(0, N, dtype=torch.bfloat16, device="cuda")
+    w = normal(gen(25), 2, N, K)
+    assert moe.grouped_mm(x, w, off, ws).shape == (0, N) and moe.grouped_mm_dgrad(dy, w, off, ws).shape == (0, K)
+    for dt in (torch.bfloat16, torch.float32):
+        out = torch.full((2, N, K), 3.0, dtype=dt, device="cuda")
+        assert (moe.grouped_mm_wgrad(dy, x, off, ws, out=out) == 0).all()
+    out = torch.full((2, N, K), 3.0, device="cuda")
+    assert (moe.grouped_mm_wgrad(dy, x, off, ws, out=out, accumulate=True) == 3.0).all()
+    assert moe.read_status(ws) == 0
+
+
 def test_an_expert_keeps_its_infinities():
     """Inf and NaN in one expert's rows or weights reach only that expert's results."""
     counts = [5, 19, 30]

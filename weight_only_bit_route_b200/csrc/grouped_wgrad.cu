@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
     const uint32_t zr = Z > 1 ? g_cta_rank() : 0u;          // this CTA's share of a tile's rows
     const int MT = (a.out_dim + 128 * CG - 1) / (128 * CG), NTN = (a.in_dim + NT - 1) / NT;
 
-    if (warp == 4 && lane < 3) g_prefetch_map(lane == 0 ? &a.a : lane == 1 ? &a.b : &a.d);
+    if (warp == 4 && (lane == 2 || (lane < 2 && a.rows > 0))) g_prefetch_map(lane == 0 ? &a.a : lane == 1 ? &a.b : &a.d);
     if (tid == 0) {
         for (int s = 0; s < SM; s++) {
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(g_smem(&full[s])), "r"(2 * CG));
