@@ -101,7 +101,7 @@ def _check(fn, code):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 # the current stream of a device as an integer (torch.cuda.current_stream builds a Stream object: 3 us a call)
