@@ -18,18 +18,19 @@ __device__ __forceinline__ void mm_expert_rows(const int32_t* offsets, int e, in
 
 // The tiles of worker p of P, as a sequence: tile p of each round of P, in snake order (every second round runs
 // backwards) where the tiles are listed from the largest to the smallest, so that the workers' sums stay within
-// about one small tile of each other; the upper half of the workers then starts from the small end, so that
-// compute-bound and memory-bound tiles run at the same time.
+// about one small tile of each other.  meet: the upper half of the workers starts from the small end, so that
+// compute-bound and memory-bound tiles run at the same time (at the price of reading a large expert's weights twice).
 struct MmSequence {
     int p, P, count;
-    bool snake;
-    __device__ __forceinline__ MmSequence(int p_, int P_, int ntiles, bool snake_) : p(p_), P(P_), snake(snake_) {
+    bool snake, back;
+    __device__ __forceinline__ MmSequence(int p_, int P_, int ntiles, bool snake_, bool meet)
+        : p(p_), P(P_), snake(snake_), back(meet && p_ >= P_ / 2) {
         const int full = ntiles / P, rem = ntiles - full * P;
         count = full + (at(full) < rem ? 1 : 0);
     }
     __device__ __forceinline__ int at(int round) const { return snake && (round & 1) ? P - 1 - p : p; }
     __device__ __forceinline__ int tile(int i) const {
-        const int round = snake && p >= P / 2 ? count - 1 - i : i;
+        const int round = back ? count - 1 - i : i;
         return round * P + at(round);
     }
 };

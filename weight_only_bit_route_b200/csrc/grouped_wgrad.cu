@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
 
     const uint32_t tmem = s_tmem;
     const int per_e = MT * NTN;
-    const MmSequence seq(int(blockIdx.x) / (CG * Z), int(gridDim.x) / (CG * Z), a.E * per_e, kSort);
+    const MmSequence seq(int(blockIdx.x) / (CG * Z), int(gridDim.x) / (CG * Z), a.E * per_e, kSort, false);
     struct Tile { int e, base, n, m0, n0; };                // base, n: the rows this CTA sums
     auto tile_of = [&](int tile) {
         Tile t;
