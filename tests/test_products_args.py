@@ -32,7 +32,7 @@ def test_product_argument_errors(call, row_args, big):
     for name in row_args:
         assert call(**{name: None}) == INVALID
         assert call(**{name: MIS}) == INVALID
-    for bad in (dict(E=1025), dict(out=60), dict(inn=12)):
+    for bad in (dict(E=1025), dict(out=60), dict(inn=12), dict(rows=2 ** 31 - 1)):
         assert call(**bad) == UNSUPPORTED, bad
     for bad in (dict(ws=None), dict(ws=P(0x10080)), dict(wsb=1023)):
         assert call(**bad) == WORKSPACE, bad

@@ -112,6 +112,7 @@ bool i8_int4(const GemvProblem& p, int rows) {
 // are no more tokens than rows).
 constexpr int64_t kInt8TwoStep = int64_t(1) << 24;       // codes from which the copy pays for its launch
 int run_int8(const GemvProblem& p, bool gateup, int rows, int ntok, void* prep, cudaStream_t s) {
+    if (rows > kMmMaxRows) return MOE_ERR_UNSUPPORTED;
     uint8_t* base = reinterpret_cast<uint8_t*>(prep);
     float* scales = reinterpret_cast<float*>(base);
     const bool two = gateup && rows >= 2 * ntok && int64_t(rows) * p.in_dim >= kInt8TwoStep;
@@ -523,7 +524,7 @@ namespace {
 int check_mm(const void* r0, const void* r1, const void* big, const int32_t* offsets, int rows, int E, int out, int in,
              void* ws, size_t ws_bytes) {
     if (rows < 0 || E <= 0 || out <= 0 || in <= 0) return MOE_ERR_INVALID_ARG;
-    if (E > kMaxE || out % 8 || in % 8) return MOE_ERR_UNSUPPORTED;
+    if (E > kMaxE || out % 8 || in % 8 || rows > kMmMaxRows) return MOE_ERR_UNSUPPORTED;
     if (!offsets || !big || !al16(big)) return MOE_ERR_INVALID_ARG;
     if (rows > 0 && (!r0 || !r1 || !al16(r0) || !al16(r1))) return MOE_ERR_INVALID_ARG;
     return check_ws(ws, ws_bytes, kStepScratch);

@@ -16,11 +16,16 @@
 // them; every role computes it from a table of the experts' first tiles in shared memory, so nothing is handed out
 // through the workspace.  Warp roles:
 //   warps 0, 3 TMA producers of A and B.  A stage is SL slices of K = 128 bytes (64 elements of 16 bits, 128 of 8)
-//              of A and B, 128-byte swizzled; rows past the tensors' ends arrive as zeros, and so does K past its end on both sides.
+//              of A and B, 128-byte swizzled; rows past the tensors' ends arrive as zeros, and so does K past its
+//              end on both sides.
 //   warp 1     issues the MMAs (in a pair: the first CTA's warp, for both) and commits each stage.
 //   warps 4-11 epilogue from tensor memory: lane = feature, column = row.  Two accumulator buffers, so that the
 //              epilogue of a tile overlaps the next tile's products.
 // B's rows behind the tile's last are other experts' rows: their columns are computed and never stored.
+//
+// Bound by the weight stream up to some hundred rows per expert (352 experts of 4096 x 1536: 8 tokens 117 us in bf16,
+// 114 us for int8 gate and up, 6.3 and 6.5 TB/s; 2048 tokens 682 us, 6.8 TB/s), by the tensor pipe and the power cap
+// above (65,536 rows over 44 experts: 1360 TFLOP/s in a burst, 1150 sustained at 1.1 to 1.2 GHz, the pipe 83 % active).
 //
 // Every wait is bounded (moe_set_wait_limit).  On expiry the kernel records MOE_ERR_TIMEOUT, stops issuing work,
 // waits (bounded) for its copies and MMAs in flight, frees its tensor memory and returns.
@@ -591,7 +596,7 @@ static int mm_launch(const MmArgs& a, cudaStream_t s) {
     int sms = 0;
     const int rc = mm_kernel_ready(reinterpret_cast<const void*>(k), kSmem, &sms);
     if (rc != MOE_OK) return rc;
-    // (clusters of 4 or 8: the tiles' own number, since not every SM can hold one)
+    // (split K: as many clusters as there are tiles, if they fit)
     const int cl = SPLIT ? a.split : CG, grid = SPLIT ? std::max(1, std::min(a.split_tiles, sms / cl)) * cl : sms / cl * cl;
     return mm_launch_cfg(k, dim3(grid), dim3(MM_THREADS), kFixed + 16 * a.E, cl, s, a);
 }
@@ -618,7 +623,8 @@ static int mm_split(const MmProblem& p, int* tiles) {
     const int64_t t = mm_row_blocks(p, 64) * ((mm_mdim(p) + 127) / 128);
     const int bk = (p.i8 ? 128 : 64) * mm_slices(p), ks = (kdim + bk - 1) / bk;
     int z = 1;
-    while (z < (p.w1 ? 4 : 8) && t * 2 * z <= 148 && ks >= 4 * z && int64_t(2 * z - 1) * ((ks + 2 * z - 1) / (2 * z)) < ks) z *= 2;
+    const int most[] = {148, 148, 132, 120};         // SMs that clusters of 1, 2, 4 and 8 can fill at once
+    for (int i = 1; z < (p.w1 ? 4 : 8) && t * 2 * z <= most[i] && ks >= 4 * z && int64_t(2 * z - 1) * ((ks + 2 * z - 1) / (2 * z)) < ks; i++) z *= 2;
     *tiles = int(std::min<int64_t>(t, 1 << 20));
     return z;
 }

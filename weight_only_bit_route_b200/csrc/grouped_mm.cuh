@@ -5,6 +5,8 @@
 
 namespace moe {
 
+constexpr int kMmMaxRows = INT32_MAX - 1024;     // a tile's row numbers stay 32-bit
+
 // The rows of expert e: [base, base + n).  Offsets outside [0, rows] or decreasing are clipped and recorded, so
 // that no index derived from them leaves the rows.
 __device__ __forceinline__ void mm_expert_rows(const int32_t* offsets, int e, int rows, int32_t* status, int& base,

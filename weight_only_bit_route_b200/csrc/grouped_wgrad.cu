@@ -16,6 +16,10 @@
 // clips at the tensor's edges.  The tensor core's fp32 sums are cut off rather than rounded, an error that grows with
 // the number of rows; so only 512 rows are summed in tensor memory at a time, and the epilogue adds those partial
 // sums in fp32 registers, rounded to nearest (a 65,536-row batch over 44 experts: 4.4e-6 of the result in one sum).
+//
+// Bound by the writes when experts hold few rows (352 experts of 47 rows, 4096 x 1536, bf16: 846 us, 5.2 TB/s written),
+// by the operands' latency and the power cap when they hold many (65,536 rows over 44 experts, fp32: 751 us in a
+// burst, 1100 TFLOP/s, the tensor pipe 68 % active).
 #include <algorithm>
 #include <cstring>
 
@@ -549,9 +553,10 @@ int launch_grouped_wgrad(const WgradProblem& p, cudaStream_t s) {
     // Few rows per expert: the tiles are short and the writes bound them, single CTAs keep more of them in flight
     // (4096 x 1536, bf16: 352 experts of 47 rows 849 us against 985 in pairs; 44 of 372 rows 285 against 291; 44 of
     // 1490 rows 852 against 686).
-    // Few tiles and many rows: clusters of four share a tile's rows.
+    // Few tiles (33 clusters of four run at once) and many rows: clusters of four share a tile's rows (one expert of
+    // 8192 rows, 1000 x 264: 29 us).
     const int64_t tiles = int64_t(p.E) * ((a.out_dim + 127) / 128) * ((a.in_dim + 255) / 256);
-    if (tiles * 4 <= 148 && p.rows >= 512 * int64_t(p.E)) return wg_launch<256, 1, 4>(a, s);
+    if (tiles * 4 <= 132 && p.rows >= 512 * int64_t(p.E)) return wg_launch<256, 1, 4>(a, s);
     return p.rows <= 512 * int64_t(p.E) || a.out_dim <= 128 ? wg_launch<256, 1, 1>(a, s) : wg_launch<256, 2, 1>(a, s);
 }
 

@@ -190,9 +190,7 @@ def workspace(T, H, E, F, top_k, device="cuda"):
 
 def control_block(device="cuda"):
     """A workspace for the calls that need no more than the control block (the 16-bit products)."""
-    ws = torch.empty(1024, dtype=torch.uint8, device=device)
-    _check("moe_workspace_init", lib.moe_workspace_init(_ptr(ws), 1024, _stream()))
-    return ws
+    return torch.zeros(1024, dtype=torch.uint8, device=device)
 
 
 def launch_count():
@@ -271,7 +269,7 @@ def _mm_check(fn, a, b, offsets, ws, shapes_ok, shapes):
     if not (b.dtype is dt and (dt is torch.bfloat16 or dt is torch.float16) and dev >= 0 and b.get_device() == dev
             and offsets.get_device() == dev and ws.get_device() == dev and a.is_contiguous() and b.is_contiguous()
             and offsets.is_contiguous() and ws.is_contiguous() and offsets.dtype is torch.int32 and offsets.dim() == 1
-            and offsets.numel() >= 2 and ws.dtype is torch.uint8 and shapes_ok):
+            and offsets.numel() >= 2 and ws.dtype is torch.uint8 and shapes_ok and max(a.shape) < 2 ** 31):
         raise MoEError(f"{fn}: needs {shapes} of one type (bf16 or fp16), offsets int32 [E+1] and a uint8 workspace, "
                        "all contiguous and on one CUDA device", -1)
     return dev
