@@ -109,13 +109,16 @@ _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_get
     lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream():
     return _raw_stream(torch.cuda.current_device())
 
 
 def _on(dev, fn, call, *args):
     """The call with the tensors' device current, on its current stream."""
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         code = call(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
@@ -263,21 +266,23 @@ def grouped_down(h_perm, offsets, row_slot, topk_w, down, ws, out=None):
     return y
 
 
+_BF16, _F16, _F32, _I32, _U8 = torch.bfloat16, torch.float16, torch.float32, torch.int32, torch.uint8
+
+
 def _mm_check(fn, a, b, offsets, ws, shapes_ok, shapes):
     """Checks what the C entry cannot see: types, agreement of the shapes, contiguity, one device."""
     dt, dev = a.dtype, a.get_device()
-    if not (b.dtype is dt and (dt is torch.bfloat16 or dt is torch.float16) and dev >= 0 and b.get_device() == dev
-            and offsets.get_device() == dev and ws.get_device() == dev and a.is_contiguous() and b.is_contiguous()
-            and offsets.is_contiguous() and ws.is_contiguous() and offsets.dtype is torch.int32 and offsets.dim() == 1
-            and offsets.numel() >= 2 and ws.dtype is torch.uint8 and shapes_ok and max(a.shape) < 2 ** 31):
-        raise MoEError(f"{fn}: needs {shapes} of one type (bf16 or fp16), offsets int32 [E+1] and a uint8 workspace, "
-                       "all contiguous and on one CUDA device", -1)
-    return dev
+    if (shapes_ok and (dt is _BF16 or dt is _F16) and b.dtype is dt and offsets.dtype is _I32 and ws.dtype is _U8
+            and dev >= 0 and b.get_device() == dev and offsets.get_device() == dev and ws.get_device() == dev
+            and a.is_contiguous() and b.is_contiguous() and offsets.is_contiguous() and ws.is_contiguous()):
+        return dev
+    raise MoEError(f"{fn}: needs {shapes} of one type (bf16 or fp16), offsets int32 [E+1] and a uint8 workspace, "
+                   "all contiguous and on one CUDA device", -1)
 
 
 def _mm_out(fn, out, shape, dtype, like):
     if out is None:
-        return like.new_empty(shape, dtype=dtype)
+        return like.new_empty(shape, dtype=dtype) if dtype is not like.dtype else like.new_empty(shape)
     if not (tuple(out.shape) == shape and out.dtype is dtype and out.device == like.device and out.is_contiguous()):
         raise MoEError(f"{fn}: out must be contiguous {dtype} {shape} on the tensors' device", -1)
     return out
@@ -286,25 +291,25 @@ def _mm_out(fn, out, shape, dtype, like):
 def grouped_mm(x, w, offsets, ws, out=None):
     """y[r] = w[e] x[r] for the rows r of each expert e (bf16 or fp16): x [rows, in], w [E, out, in] -> [rows, out].
     Rows outside every expert are not written."""
-    fn = "moe_grouped_mm"
-    sx, sw = x.shape, w.shape
-    dev = _mm_check(fn, x, w, offsets, ws, len(sx) == 2 and len(sw) == 3 and sw[0] == offsets.numel() - 1
-                    and sw[2] == sx[1], "x [rows, in], w [E, out, in]")
-    y = _mm_out(fn, out, (sx[0], sw[1]), x.dtype, x)
-    _on(dev, fn, lib.moe_grouped_mm, x.data_ptr(), offsets.data_ptr(), sx[0], w.data_ptr(), sw[0], sw[1], sw[2],
-        x.dtype is torch.float16, y.data_ptr(), ws.data_ptr(), ws.numel())
+    sx, sw, so = x.shape, w.shape, offsets.shape
+    ok = len(sx) == 2 and len(sw) == 3 and len(so) == 1 and sw[0] == so[0] - 1 and sw[2] == sx[1] and sx[0] < 1 << 31
+    dev = _mm_check("moe_grouped_mm", x, w, offsets, ws, ok, "x [rows, in], w [E, out, in]")
+    rows, (E, n_out, n_in) = sx[0], sw
+    y = _mm_out("moe_grouped_mm", out, (rows, n_out), x.dtype, x)
+    _on(dev, "moe_grouped_mm", lib.moe_grouped_mm, x.data_ptr(), offsets.data_ptr(), rows, w.data_ptr(), E, n_out, n_in,
+        x.dtype is _F16, y.data_ptr(), ws.data_ptr(), ws.numel())
     return y
 
 
 def grouped_mm_dgrad(dy, w, offsets, ws, out=None):
     """Gradient of grouped_mm by x: dx[r] = w[e]^T dy[r]; dy [rows, out], w [E, out, in] -> [rows, in]."""
-    fn = "moe_grouped_mm_dgrad"
-    sy, sw = dy.shape, w.shape
-    dev = _mm_check(fn, dy, w, offsets, ws, len(sy) == 2 and len(sw) == 3 and sw[0] == offsets.numel() - 1
-                    and sw[1] == sy[1], "dy [rows, out], w [E, out, in]")
-    dx = _mm_out(fn, out, (sy[0], sw[2]), dy.dtype, dy)
-    _on(dev, fn, lib.moe_grouped_mm_dgrad, dy.data_ptr(), offsets.data_ptr(), sy[0], w.data_ptr(), sw[0], sw[1], sw[2],
-        dy.dtype is torch.float16, dx.data_ptr(), ws.data_ptr(), ws.numel())
+    sy, sw, so = dy.shape, w.shape, offsets.shape
+    ok = len(sy) == 2 and len(sw) == 3 and len(so) == 1 and sw[0] == so[0] - 1 and sw[1] == sy[1] and sy[0] < 1 << 31
+    dev = _mm_check("moe_grouped_mm_dgrad", dy, w, offsets, ws, ok, "dy [rows, out], w [E, out, in]")
+    rows, (E, n_out, n_in) = sy[0], sw
+    dx = _mm_out("moe_grouped_mm_dgrad", out, (rows, n_in), dy.dtype, dy)
+    _on(dev, "moe_grouped_mm_dgrad", lib.moe_grouped_mm_dgrad, dy.data_ptr(), offsets.data_ptr(), rows, w.data_ptr(), E,
+        n_out, n_in, dy.dtype is _F16, dx.data_ptr(), ws.data_ptr(), ws.numel())
     return dx
 
 
@@ -312,18 +317,18 @@ def grouped_mm_wgrad(dy, x, offsets, ws, out=None, out_dtype=None, accumulate=Fa
     """Gradient of grouped_mm by w: dw[e] = sum over e's rows of dy[r] x[r]^T -> [E, out, in], in the tensors'
     type or fp32.  accumulate: add to `out` (fp32) instead."""
     fn = "moe_grouped_mm_wgrad"
-    sy, sx = dy.shape, x.shape
-    dev = _mm_check(fn, dy, x, offsets, ws, len(sy) == 2 and len(sx) == 2 and sy[0] == sx[0],
-                    "dy [rows, out], x [rows, in]")
+    sy, sx, so = dy.shape, x.shape, offsets.shape
+    ok = len(sy) == 2 and len(sx) == 2 and len(so) == 1 and so[0] >= 2 and sy[0] == sx[0] and sx[0] < 1 << 31
+    dev = _mm_check(fn, dy, x, offsets, ws, ok, "dy [rows, out], x [rows, in]")
     dt = out_dtype or (out.dtype if out is not None else dy.dtype)
-    if dt is not torch.float32 and dt is not dy.dtype:
+    if dt is not _F32 and dt is not dy.dtype:
         raise MoEError(f"{fn}: out_dtype is the tensors' type or float32", -1)
     if accumulate and out is None:
         raise MoEError(f"{fn}: accumulate needs out", -1)
-    E = offsets.numel() - 1
-    dw = _mm_out(fn, out, (E, sy[1], sx[1]), dt, dy)
-    _on(dev, fn, lib.moe_grouped_mm_wgrad, dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), sy[0], E, sy[1], sx[1],
-        dy.dtype is torch.float16, dw.data_ptr(), dt is torch.float32, bool(accumulate), ws.data_ptr(), ws.numel())
+    rows, n_out, n_in, E = sy[0], sy[1], sx[1], so[0] - 1
+    dw = _mm_out(fn, out, (E, n_out, n_in), dt, dy)
+    _on(dev, fn, lib.moe_grouped_mm_wgrad, dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), rows, E, n_out, n_in,
+        dy.dtype is _F16, dw.data_ptr(), dt is _F32, bool(accumulate), ws.data_ptr(), ws.numel())
     return dw
 
 
