@@ -125,6 +125,27 @@ def test_few_tiles_share_a_long_contraction(counts, K, N):
         assert torch.equal(moe.grouped_mm(x, w, off, ws)[:sum(counts)], y[:sum(counts)])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("K,N", [(520, 1528), (512, 1536)])
+@pytest.mark.parametrize("counts", [[700, 0, 129, 300], [15, 513, 0, 1024], [2, 3, 4, 640]], ids=str)
+def test_weight_gradients_of_many_rows(counts, K, N, dtype):
+    """Sizes that run on CTA pairs: several partial sums of 512 rows, ragged ends, experts without rows."""
+    dt, E, rows = TYPES[dtype], len(counts), sum(counts) + 40
+    g = gen(26)
+    x, dy = normal(g, rows, K, dtype=dt), normal(g, rows, N, dtype=dt, std=0.5)
+    x[sum(counts):], dy[sum(counts):] = float("inf"), float("nan")
+    off, ws = offsets_of(counts), moe.control_block()
+    base = normal(g, E, N, K, dtype=torch.float32)
+    dw, dwf = moe.grouped_mm_wgrad(dy, x, off, ws), moe.grouped_mm_wgrad(dy, x, off, ws, out_dtype=torch.float32)
+    acc = moe.grouped_mm_wgrad(dy, x, off, ws, out=base.clone(), accumulate=True)
+    assert moe.read_status(ws) == 0
+    for e, a, b in spans(counts):
+        xe, de = x[a:b].double(), dy[a:b].double()
+        ref, mag = de.T @ xe, de.abs().T @ xe.abs()
+        for got, want in ((dw[e], ref), (dwf[e], ref), (acc[e], ref + base[e].double())):
+            assert ((got.double() - want).abs() <= product_bound(mag, b - a, want, got.dtype)).all(), (e, got.dtype)
+
+
 def test_no_rows_at_all():
     """Empty row tensors: nothing to multiply, a zero gradient, an accumulated one left as it was."""
     off, ws, K, N = offsets_of([0, 0]), moe.control_block(), 72, 136
@@ -619,7 +640,7 @@ def _large_calls():
     rows = sum(counts)
     x, dy, w = normal(g, rows, 520), normal(g, rows, 392), normal(g, 4, 392, 520)
     xs, ws_ = normal(g, 63, 2048), normal(g, 2, 136, 2048)
-    xl, dyl, offl = normal(g, 601, 1024), normal(g, 601, 1536), offsets_of([601])
+    xl, dyl, offl = normal(g, 601, 2048), normal(g, 601, 1536), offsets_of([601])
     off, offs, rs = offsets_of(counts), offsets_of(few), routing(counts, k, g)
     x8 = normal(g, rows // k, H)
     gate, up, down = int8_bank(g, 4, F, H), int8_bank(g, 4, F, H), int8_bank(g, 4, H, F)

@@ -550,14 +550,15 @@ int launch_grouped_wgrad(const WgradProblem& p, cudaStream_t s) {
     a.f16 = p.f16;
     a.out_f32 = p.out_f32;
     a.accumulate = p.accumulate;
-    // Few rows per expert: the tiles are short and the writes bound them, single CTAs keep more of them in flight
-    // (4096 x 1536, bf16: 352 experts of 47 rows 849 us against 985 in pairs; 44 of 372 rows 285 against 291; 44 of
-    // 1490 rows 852 against 686).
     // Few tiles (33 clusters of four run at once) and many rows: clusters of four share a tile's rows (one expert of
     // 8192 rows, 1000 x 264: 29 us).
     const int64_t tiles = int64_t(p.E) * ((a.out_dim + 127) / 128) * ((a.in_dim + 255) / 256);
     if (tiles * 4 <= 132 && p.rows >= 512 * int64_t(p.E)) return wg_launch<256, 1, 4>(a, s);
-    return p.rows <= 512 * int64_t(p.E) || a.out_dim <= 128 ? wg_launch<256, 1, 1>(a, s) : wg_launch<256, 2, 1>(a, s);
+    // Up to 128 rows per expert the tiles are short and the writes bound them: single CTAs keep more of them in flight;
+    // above, a pair loads a quarter less per tile.  Measured (4096 x 1536, bf16, us, single / pair): 352 experts of 47
+    // rows 836 / 1044; 44 of 93 rows 138 / 162, of 186 182 / 166, of 372 281 / 236, of 1490 852 / 686.
+    const int64_t pairs = int64_t(p.E) * ((a.out_dim + 255) / 256) * ((a.in_dim + 255) / 256);
+    return p.rows > 128 * int64_t(p.E) && pairs >= 37 ? wg_launch<256, 2, 1>(a, s) : wg_launch<256, 1, 1>(a, s);
 }
 
 }  // namespace moe
