@@ -122,8 +122,8 @@ typedef struct {
  * bf16 rounding of the routing input changed far more top-8 sets).  The router
  * and the routed experts read the fp16 x exactly; the BF16 shared expert reads x
  * rounded to bf16 (its MMA takes bf16 operands); the intermediates h and
- * y_perm stay bf16.  Requires the routed banks in a 4-bit format with both
- * projections on the tensor-core GEMM (H and F multiples of 256); from 64
+ * y_perm stay bf16.  Requires the routed banks in int8, or in a 4-bit format
+ * with both projections on the tensor-core GEMM (H and F multiples of 256); from 64
  * tokens the router logits run on the fp32 SIMT kernel (the tensor-core router
  * splits bf16 operands). */
 typedef struct {

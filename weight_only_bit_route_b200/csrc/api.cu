@@ -300,13 +300,12 @@ int layer_run(const void* x, int T, const moe_layer* L, void* y, void* ws, cudaS
     } else {
         MOE_TRY(launch_stream_gemv(gu, nullptr, true, T, prep, s, true));
     }
-    if (int8) {
-    } else if (routed_gemm) {
+    if (routed_gemm) {
         GemmBuffers db = gemm_buffers(prep, R, F, false, i8);
         db.sched = status + 8;
         db.max_expert_rows = T;
         MOE_TRY(grouped_gemm(dn, false, R, db, s));
-    } else {
+    } else if (!int8) {
         MOE_TRY(launch_stream_gemv(dn, nullptr, false, R, prep, s, true));
     }
     if (has_sh) {

@@ -605,13 +605,14 @@ static int mm_mdim(const MmProblem& p) { return p.grad ? p.in_dim : p.out_dim; }
 // About how many (expert, row block) pairs there are with blocks of nt rows
 static int64_t mm_row_blocks(const MmProblem& p, int nt) { return std::max(std::min(p.E, p.rows), (p.rows + nt - 1) / nt); }
 
-// Tiles of 256 rows x 256 features on CTA pairs when the experts hold more than 64 rows on average and half the pairs
-// get a tile; else 64 rows x 128 features on single CTAs.  Measured (4096 -> 1536, us, single / pair): 352 experts of
-// 47 rows 682 / 725 in bf16, 712 / 694 in int8 gate/up; 44 experts of 1490 rows 1122 / 629; one expert of 300 rows
+// Tiles of 256 rows x 256 features on CTA pairs when the experts hold more than 64 rows on average (int8: 32, whose
+// MMAs take half the time) and half the pairs get a tile; else 64 rows x 128 features on single CTAs.  Measured (4096
+// -> 1536, us, single / pair): 352 experts of 47 rows 682 / 725 in bf16 (Zipf load 772 / 760), int8 gate/up 721 / 711
+// (775 / 728), int8 down 368 / 375 (442 / 403); 44 experts of 1490 rows 1122 / 629; one expert of 300 rows
 // 14 / 20, of 1000 rows (24 pair tiles) 30 / 27, of 3000 57 / 29; four of 150 rows (24 pair tiles, K 2048) 11 / 14.
 // (Tiles of 16 rows were never faster than those of 64: 8 tokens over 352 experts 121 us against 117.)
 static bool mm_pair(const MmProblem& p) {
-    return p.rows > 64 * int64_t(p.E) && mm_row_blocks(p, 256) * ((mm_mdim(p) + 255) / 256) >= 37;
+    return p.rows > (p.i8 ? 32 : 64) * int64_t(p.E) && mm_row_blocks(p, 256) * ((mm_mdim(p) + 255) / 256) >= 37;
 }
 // K slices per stage: two where the stage then still fits the ring four times
 static int mm_slices(const MmProblem& p) { return p.w1 ? 1 : 2; }
