@@ -126,6 +126,32 @@ def test_few_tiles_share_a_long_contraction(counts, K, N):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("K,N", [(2056, 2040), (2048, 2048)])
+@pytest.mark.parametrize("counts", [[700, 0, 129, 300, 1], [2000, 3, 0, 1000, 500]], ids=str)
+def test_products_of_many_rows(counts, K, N, dtype):
+    """Sizes that run on CTA pairs, in both directions, with rows in front and behind that nothing may read."""
+    dt, E, first, rows = TYPES[dtype], len(counts), 5, sum(counts) + 60
+    g = gen(27)
+    x, dy, w = normal(g, rows, K, dtype=dt), normal(g, rows, N, dtype=dt), normal(g, E, N, K, dtype=dt, std=0.1)
+    end = first + sum(counts)
+    for t in (x, dy):
+        t[:first], t[end:] = float("nan"), float("inf")
+    off, ws = offsets_of(counts, first), moe.control_block()
+    y = torch.full((rows, N), 7.0, dtype=dt, device="cuda")
+    dx = torch.full((rows, K), 7.0, dtype=dt, device="cuda")
+    moe.grouped_mm(x, w, off, ws, out=y)
+    moe.grouped_mm_dgrad(dy, w, off, ws, out=dx)
+    assert moe.read_status(ws) == 0
+    for out in (y, dx):
+        assert (out[:first] == 7.0).all() and (out[end:] == 7.0).all()
+    for e, a, b in spans(counts, first):
+        we = w[e].double()
+        for got, p, q, terms in ((y[a:b], x[a:b].double(), we.T, K), (dx[a:b], dy[a:b].double(), we, N)):
+            ref = p @ q
+            assert ((got.double() - ref).abs() <= product_bound(p.abs() @ q.abs(), terms, ref, dt)).all(), e
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("K,N", [(520, 1528), (512, 1536)])
 @pytest.mark.parametrize("counts", [[700, 0, 129, 300], [15, 513, 0, 1024], [2, 3, 4, 640]], ids=str)
 def test_weight_gradients_of_many_rows(counts, K, N, dtype):
@@ -355,11 +381,12 @@ COUNTS8 = {
     "big": ([600, 0, 257, 7], 8),
     "single": ([37], 1),
     "pair": ([61, 3], 2),
+    "many": ([700, 0, 129, 300, 7], 8),
 }
 
 
 @pytest.mark.parametrize("load", list(COUNTS8))
-@pytest.mark.parametrize("H,F", [(256, 128), (1024, 384), (640, 256), (4096, 1152)])
+@pytest.mark.parametrize("H,F", [(256, 128), (1024, 384), (640, 256), (4096, 1152), (2048, 2048)])
 def test_int8_steps_match_the_formula(load, H, F):
     counts, k = COUNTS8[load]
     E, rows = len(counts), sum(counts)
@@ -579,9 +606,32 @@ def _calls(seed=13):
     return run, lambda: moe.workspace(rows // k, H, 4, F, 4)
 
 
-def test_captured_and_replayed():
-    """Two graphs captured over one workspace, replayed in turn with new inputs in place."""
-    run, new_ws = _calls()
+def _large_calls(seed=16):
+    """The same calls at sizes that run on CTA pairs, and with few tiles on clusters that share a contraction."""
+    counts, few, k, H, F = [700, 0, 300, 24], [3, 60], 8, 2560, 2560
+    g = gen(seed)
+    rows = sum(counts)
+    x, dy, w = normal(g, rows, 2600), normal(g, rows, 2568), normal(g, 4, 2568, 2600)
+    xs, ws_ = normal(g, 63, 2048), normal(g, 2, 136, 2048)
+    xl, dyl, offl = normal(g, 601, 2048), normal(g, 601, 1536), offsets_of([601])
+    off, offs, rs = offsets_of(counts), offsets_of(few), routing(counts, k, g)
+    x8 = normal(g, rows // k, H)
+    gate, up, down = int8_bank(g, 4, F, H), int8_bank(g, 4, F, H), int8_bank(g, 4, H, F)
+
+    def run(ws):
+        h = moe.grouped_swiglu(x8, off, rs, k, gate, up, rows, ws)
+        return [moe.grouped_mm(x, w, off, ws), moe.grouped_mm_dgrad(dy, w, off, ws), moe.grouped_mm_wgrad(dy, x, off, ws),
+                moe.grouped_mm_wgrad(dy, x, off, ws, out_dtype=torch.float32), moe.grouped_mm(xs, ws_, offs, ws), h,
+                moe.grouped_mm_wgrad(dyl, xl, offl, ws), moe.grouped_mm_wgrad(dyl[:, :136].contiguous(), xl, offl, ws),
+                moe.grouped_down(h, off, rs, None, down, ws)]
+
+    return run, lambda: moe.workspace(rows // k, H, 4, F, 4)
+
+
+@pytest.mark.parametrize("calls", [_calls, _large_calls], ids=["small", "large"])
+def test_captured_and_replayed(calls):
+    """Two graphs captured over one workspace, replayed in turn."""
+    run, new_ws = calls()
     ws = new_ws()
     ref = run(ws)
     side = torch.cuda.Stream()
@@ -605,9 +655,10 @@ def test_captured_and_replayed():
         gr.reset()
 
 
-def test_two_streams_and_threads():
+@pytest.mark.parametrize("calls", [_calls, _large_calls], ids=["small", "large"])
+def test_two_streams_and_threads(calls):
     """Calls on two streams from two host threads with separate workspaces: the bits of one thread."""
-    made = [_calls(s) for s in (14, 15)]
+    made = [calls(s) for s in (14, 15)]
     refs = [run(new()) for run, new in made]
     torch.cuda.synchronize()
     got, errors = [None, None], []
@@ -631,28 +682,6 @@ def test_two_streams_and_threads():
     for out, ref in zip(got, refs):
         for a, b in zip(out, ref):
             assert torch.equal(a, b)
-
-
-def _large_calls():
-    """The same calls at sizes that run on CTA pairs, and with few tiles on clusters that share a contraction."""
-    counts, few, k, H, F = [700, 0, 300, 24], [3, 60], 8, 512, 256
-    g = gen(16)
-    rows = sum(counts)
-    x, dy, w = normal(g, rows, 520), normal(g, rows, 392), normal(g, 4, 392, 520)
-    xs, ws_ = normal(g, 63, 2048), normal(g, 2, 136, 2048)
-    xl, dyl, offl = normal(g, 601, 2048), normal(g, 601, 1536), offsets_of([601])
-    off, offs, rs = offsets_of(counts), offsets_of(few), routing(counts, k, g)
-    x8 = normal(g, rows // k, H)
-    gate, up, down = int8_bank(g, 4, F, H), int8_bank(g, 4, F, H), int8_bank(g, 4, H, F)
-
-    def run(ws):
-        h = moe.grouped_swiglu(x8, off, rs, k, gate, up, rows, ws)
-        return [moe.grouped_mm(x, w, off, ws), moe.grouped_mm_dgrad(dy, w, off, ws), moe.grouped_mm_wgrad(dy, x, off, ws),
-                moe.grouped_mm_wgrad(dy, x, off, ws, out_dtype=torch.float32), moe.grouped_mm(xs, ws_, offs, ws), h,
-                moe.grouped_mm_wgrad(dyl, xl, offl, ws), moe.grouped_mm_wgrad(dyl[:, :136].contiguous(), xl, offl, ws),
-                moe.grouped_down(h, off, rs, None, down, ws)]
-
-    return run, lambda: moe.workspace(rows // k, H, 4, F, 4)
 
 
 @pytest.mark.parametrize("calls", [_calls, _large_calls], ids=["small", "large"])
