@@ -3,7 +3,7 @@
 // Rows offsets[e] to offsets[e+1] belong to expert e.  With W_e = w[e] stored [out, in]:
 //     forward   y[r, n]  = sum_k x[r, k] w[e, n, k]                     (K = in)
 //     gradient  dx[r, k] = sum_n dy[r, n] w[e, n, k]                    (K = out)
-//     int8      y[r, n]  = t s_r s_n sum_k q[r, k] w[e, n, k]           (s: row and channel scales, t: routing weight)
+//     int8      y[r, n]  = t s_r s_n sum_k q[r, k] w[e, n, k]           (s: row and channel scales; s_r holds the routing weight t)
 //     int8 gate/up       h[r, f] = silu(g) u, g and u as above with two banks
 //
 // One kernel computes them all as D = A B with A the weights (M = 128 of their output features, 256 for a CTA
@@ -86,12 +86,11 @@ struct MmArgs {
     CUtensorMap a0, a1;                  // weights [E][out][in]; a1: up (gate/up)
     CUtensorMap b[MM_BOXES];             // rows, boxes of 16, 32, 64 and 128
     const int32_t* offsets;
-    const int32_t* row_slot;             // int8: slot of a row (routing weight), nullable
-    const float* topk_w;
     const float* act_scale;              // int8: [rows]
     const float* s0; const float* s1;    // int8: channel scales [E][out]
     uint16_t* out;                       // [rows][ldo]
     int32_t* status;
+    uint32_t mt_inv;                     // 2^32 / feature tiles, rounded down
     int E, mdim, kdim, rows;             // mdim: output features (A's M), kdim: contraction length
     int f16;                             // 16-bit elements are fp16 (else bf16)
     int chunked;                         // bit 0: a0 and a1, bit 1: b see K (gradient: A's features) in 128-byte chunks
@@ -190,7 +189,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
 
     uint8_t* ring = smem + ((1024u - (g_smem(smem) & 1023u)) & 1023u);
     uint8_t* red = ring + S * C::kStage;             // split K: [other CTA][own block][matrix][4][128 lanes] of 16 bytes
-    int4* tbl = reinterpret_cast<int4*>(red + C::kRedBytes);        // active experts: {expert, first tile, first row, rows}
+    int4* tbl = reinterpret_cast<int4*>(red + C::kRedBytes);        // active experts: {expert | rows per tile << 16, first tile, first row, rows}
     constexpr bool kSort = CG == 2;                  // large batches: the experts' tiles from the most rows to the fewest
     constexpr int PER = (kMaxE + MM_THREADS - 1) / MM_THREADS;
     if constexpr (kSort) {
@@ -245,7 +244,12 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
         int pos = base + v - local, tpos = tbase + w - ltiles;
 #pragma unroll
         for (int i = 0; i < PER; i++)
-            if (ne[i] > 0) { tbl[pos] = make_int4(ex[i], tpos, eb[i], ne[i]); pos++; tpos += nt[i]; }
+            if (ne[i] > 0) {
+                const int row_tiles = (ne[i] + NT - 1) / NT, per = (ne[i] + row_tiles - 1) / row_tiles;
+                tbl[pos] = make_int4(ex[i] | (per << 16), tpos, eb[i], ne[i]);
+                pos++;
+                tpos += nt[i];
+            }
         if (tid == 0) { s_nact = tot; s_total = ttot; }
     }
     g_fence_before();
@@ -256,21 +260,20 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
     const uint32_t tmem = s_tmem;
     const int nact = s_nact;
     const MmSequence seq(int(blockIdx.x) / (CG * z), int(gridDim.x) / (CG * z), s_total, kSort, a.meet != 0);
+    // (by whole warps, once per tile and role: with short contractions a tile takes no more than some thousand cycles,
+    // so the expert is found by two votes and nothing is divided)
     auto tile_of = [&](int tile) {
-        int lo = 0, hi = nact - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (tbl[mid].y <= tile) lo = mid; else hi = mid - 1;
-        }
+        int lo = 0;
+        if (nact > 32) lo = 32 * (__popc(__ballot_sync(0xffffffffu, 32 * lane < nact && tbl[min(32 * lane, nact - 1)].y <= tile)) - 1);
+        lo += __popc(__ballot_sync(0xffffffffu, lo + lane < nact && tbl[min(lo + lane, nact - 1)].y <= tile)) - 1;
         const int4 te = tbl[lo];
         MmTile t;
-        t.e = te.x;
-        const int local = tile - te.y, n_e = te.w;
-        const int ntile = (n_e + NT - 1) / NT;
-        const int per = (n_e + ntile - 1) / ntile;                 // balanced rows per tile
+        t.e = te.x & 0xffff;
+        const int local = tile - te.y, n_e = te.w, per = te.x >> 16;   // balanced rows per tile
         // the features of a row block run fastest: the CTAs of a wave share the rows, and the expert's
         // weights stay in L2 from one row block to the next
-        const int n = local / MT;
+        int n = int(__umulhi(uint32_t(local), a.mt_inv));              // local / MT, or one less
+        n += (n + 1) * MT <= local ? 1 : 0;
         t.m0 = (local - n * MT) * (128 * CG);
         t.nval = min(per, n_e - n * per);
         t.n0 = te.z + n * per;
@@ -426,32 +429,38 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
         constexpr int kScaleRegs = I8 ? (NT + 63) / 64 : 1;
         MmHalves use;
         bool ok = true;
-        for (int ti = 0; ti < seq.count && !g_aborted(&s_ab); ti++) {
-            const MmTile T = tile_of(seq.tile(ti));
-            const int m = T.m0 + int(rank) * 128 + q * 32 + lane;            // my feature
-            const bool mine = m < a.mdim;
-            float w0 = 0.f, w1 = 0.f;
-            float rs[kScaleRegs];                                             // the scales of my blocks' rows
+        // A tile's coordinates and scales, on their way while the tile before is written
+        struct Pre {
+            MmTile T;
+            float w0, w1, rs[kScaleRegs];                                     // my feature's scales, my blocks' rows'
+        };
+        auto fetch = [&](int ti) {
+            Pre p;
+            p.T = tile_of(seq.tile(ti));
+            const int m = p.T.m0 + int(rank) * 128 + q * 32 + lane;
+            p.w0 = p.w1 = 0.f;
             if (I8) {
-                if (mine) {
-                    w0 = a.s0[size_t(T.e) * a.mdim + m];
-                    if (GU) w1 = a.s1[size_t(T.e) * a.mdim + m];
+                if (m < a.mdim) {
+                    p.w0 = a.s0[size_t(p.T.e) * a.mdim + m];
+                    if (GU) p.w1 = a.s1[size_t(p.T.e) * a.mdim + m];
                 }
 #pragma unroll
                 for (int i = 0; i < kScaleRegs; i++) {
                     const int c = (4 * i + 2 * (lane >> 4) + hsel) * 16 + (lane & 15);   // lanes 0-15: block 2i, 16-31: 2i + 1
-                    rs[i] = 0.f;
-                    if (c < T.nval) {
-                        const int r = T.n0 + c;
-                        rs[i] = a.act_scale[r];
-                        if (!GU && a.topk_w) {
-                            const int slot = a.row_slot[r];
-                            if (slot >= 0 && slot < a.rows) rs[i] *= a.topk_w[slot];
-                            else { set_status(a.status, MOE_ERR_DEVICE_INDEX); rs[i] = 0.f; }
-                        }
-                    }
+                    p.rs[i] = c < p.T.nval ? a.act_scale[p.T.n0 + c] : 0.f;
                 }
             }
+            return p;
+        };
+        Pre next;
+        if (seq.count > 0) next = fetch(0);
+        for (int ti = 0; ti < seq.count && !g_aborted(&s_ab); ti++) {
+            const Pre cur = next;
+            const MmTile& T = cur.T;
+            const int m = T.m0 + int(rank) * 128 + q * 32 + lane;            // my feature
+            const bool mine = m < a.mdim;
+            const float w0 = cur.w0, w1 = cur.w1;
+            const float (&rs)[kScaleRegs] = cur.rs;
             const bool both = T.bn > C::kHalfRows;
             const uint32_t h = both ? 0 : use.next;
             if (!g_wait_long(g_smem(&acc_full[h]), use.uses(h) & 1, &s_ab) ||
@@ -460,6 +469,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
                 break;
             }
             g_fence_after();
+            if (ti + 1 < seq.count) next = fetch(ti + 1);
             const uint32_t acc = tmem + lane_addr + h * C::kHalfCols, up = both ? NT : C::kHalfRows;
             uint16_t* dst = a.out + size_t(T.n0 + odd) * a.mdim + (m - odd);
             if constexpr (SPLIT) {
@@ -666,8 +676,6 @@ int launch_grouped_mm(const MmProblem& p, cudaStream_t s) {
                 : g_map(&a.b[i], !p.i8, p.act, kdim, p.rows, uint64_t(kdim) * el, bk, 16u << i, true);
     if (rc != MOE_OK) return rc;
     a.offsets = p.offsets;
-    a.row_slot = p.row_slot;
-    a.topk_w = p.topk_w;
     a.act_scale = p.act_scale;
     a.s0 = p.s0;
     a.s1 = p.s1;
@@ -679,6 +687,8 @@ int launch_grouped_mm(const MmProblem& p, cudaStream_t s) {
     a.rows = p.rows;
     a.f16 = p.f16;
     a.early = p.i8;
+    const uint32_t mt = uint32_t(a.mdim + (pair ? 255 : 127)) / (pair ? 256u : 128u);
+    a.mt_inv = mt > 1 ? uint32_t((uint64_t(1) << 32) / mt) : 0xffffffffu;
     if (pair) {
         // Experts of some hundred rows or fewer on average: the small ones' tiles wait for memory beside the large
         // ones' (65,536 rows, Zipf over 352 experts, int8 gate/up: 1096 us against 1171; over 44 experts the weights

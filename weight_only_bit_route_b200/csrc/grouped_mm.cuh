@@ -54,10 +54,8 @@ struct MmProblem {
     const void* act;             // rows of the contraction: x or codes [rows, in], dy [rows, out] (grad)
     const void* w0; const void* w1;      // weights [E, out, in]; w1: up (int8 gate/up), else null
     const float* s0; const float* s1;    // int8: channel scales [E, out]
-    const float* act_scale;              // int8: row scales [rows]
+    const float* act_scale;              // int8: row scales [rows], times the routing weight
     const int32_t* offsets;              // [E + 1]
-    const int32_t* row_slot;             // int8: [rows], for topk_w
-    const float* topk_w;                 // int8: weight by slot, nullable
     uint16_t* out;                       // [rows, out], [rows, in] (grad)
     int32_t* status;
     int E, out_dim, in_dim, rows;
@@ -75,11 +73,12 @@ struct WgradProblem {
 };
 int launch_grouped_wgrad(const WgradProblem& p, cudaStream_t s);
 
-// Rows to 8 bits: codes [rows, cols], scales [rows].  With row_slot, row r reads row row_slot[r] / top_k of the
-// nsrc rows of x; with nrows (device), rows from *nrows on are left alone.  status nullable.
+// Rows to 8 bits: codes [rows, cols], scales [rows].  With row_slot and top_k, row r reads row row_slot[r] / top_k of
+// the nsrc rows of x; with row_slot and row_w (one or the other), the scale is multiplied by row_w[row_slot[r]], slots
+// below rows.  With nrows (device), rows from *nrows on are left alone.  status nullable.
 int launch_quant_int8(const void* x, bool f16, int64_t rows, int64_t cols, const int32_t* row_slot, int top_k,
-                      int64_t nsrc, const int32_t* nrows, int8_t* codes, float* scales, int32_t* status,
-                      cudaStream_t s);
+                      int64_t nsrc, const float* row_w, const int32_t* nrows, int8_t* codes, float* scales,
+                      int32_t* status, cudaStream_t s);
 // Rows of codes and their scales by slot, as above, from the nsrc rows src, src_scales.
 int launch_gather_int8(const int8_t* src, const float* src_scales, int rows, int cols, const int32_t* row_slot, int top_k,
                        int nsrc, const int32_t* nrows, int8_t* codes, float* scales, int32_t* status, cudaStream_t s);

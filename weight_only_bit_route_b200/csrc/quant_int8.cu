@@ -46,7 +46,8 @@ __device__ __forceinline__ long long q8_source(int slot, int top_k, long long ns
 template <bool F16, int TPR>           // TPR threads per row: 32 or the block
 __global__ void __launch_bounds__(Q8_THREADS) quant_int8_kernel(const uint16_t* __restrict__ x, long long cols,
                                                                const int32_t* __restrict__ row_slot, int top_k,
-                                                               long long nsrc, const int32_t* __restrict__ nrows,
+                                                               long long nsrc, const float* __restrict__ row_w,
+                                                               const int32_t* __restrict__ nrows,
                                                                int8_t* __restrict__ codes, float* __restrict__ scales,
                                                                int32_t* status, long long rows) {
     constexpr int kKeep = TPR == 32 ? 8 : 4;                          // 16-byte chunks per thread kept in registers
@@ -57,7 +58,15 @@ __global__ void __launch_bounds__(Q8_THREADS) quant_int8_kernel(const uint16_t* 
     if (row >= rows || (nrows && row >= *nrows)) return;                               // behind the last expert's rows
     const long long n = cols / 8;
     uint2* dst = reinterpret_cast<uint2*>(codes + row * cols);
-    const long long src = row_slot ? q8_source(row_slot[row], top_k, nsrc) : row;
+    long long src = row;
+    float weight = 1.f;
+    if (row_w) {
+        const int slot = row_slot[row];
+        if (slot >= 0 && slot < rows) weight = row_w[slot];
+        else src = -1;
+    } else if (row_slot) {
+        src = q8_source(row_slot[row], top_k, nsrc);
+    }
     if (src < 0) {                                                    // a slot out of range: a zero row
         if (tid == 0) {
             scales[row] = 0.f;
@@ -88,7 +97,7 @@ __global__ void __launch_bounds__(Q8_THREADS) quant_int8_kernel(const uint16_t* 
     const bool bad = m >= (F16 ? 0x7c00u : 0x7f80u);
     const float amax = act_lo<F16>(m);
     if (tid == 0) {
-        scales[row] = bad ? __int_as_float(0x7fffffff) : __fdiv_rn(amax, 127.f);
+        scales[row] = bad ? __int_as_float(0x7fffffff) : __fdiv_rn(amax, 127.f) * weight;
         if (bad && status) set_status(status, MOE_ERR_NONFINITE);
     }
     const bool zero = bad || m == 0;
@@ -123,15 +132,15 @@ __global__ void __launch_bounds__(Q8_THREADS) quant_int8_kernel(const uint16_t* 
 }
 
 int launch_quant_int8(const void* x, bool f16, int64_t rows, int64_t cols, const int32_t* row_slot, int top_k,
-                      int64_t nsrc, const int32_t* nrows, int8_t* codes, float* scales, int32_t* status,
-                      cudaStream_t s) {
+                      int64_t nsrc, const float* row_w, const int32_t* nrows, int8_t* codes, float* scales,
+                      int32_t* status, cudaStream_t s) {
     if (rows <= 0) return MOE_OK;
     const bool warp = rows >= Q8_WARP_ROWS && cols <= Q8_WARP_COLS;
     auto k = warp ? (f16 ? quant_int8_kernel<true, 32> : quant_int8_kernel<false, 32>)
                   : (f16 ? quant_int8_kernel<true, Q8_THREADS> : quant_int8_kernel<false, Q8_THREADS>);
     const int64_t blocks = warp ? (rows + Q8_THREADS / 32 - 1) / (Q8_THREADS / 32) : rows;
     return mm_launch_cfg(k, dim3(unsigned(blocks)), dim3(Q8_THREADS), 0, 1, s, static_cast<const uint16_t*>(x),
-                         (long long)cols, row_slot, top_k, (long long)nsrc, nrows, codes, scales, status, (long long)rows);
+                         (long long)cols, row_slot, top_k, (long long)nsrc, row_w, nrows, codes, scales, status, (long long)rows);
 }
 
 // One block per row, 16 bytes per thread and step.
