@@ -90,7 +90,7 @@ struct MmArgs {
     const float* s0; const float* s1;    // int8: channel scales [E][out]
     uint16_t* out;                       // [rows][ldo]
     int32_t* status;
-    uint32_t mt_inv;                     // 2^32 / feature tiles, rounded down
+    uint32_t mt_inv;                     // mm_inverse(feature tiles)
     int E, mdim, kdim, rows;             // mdim: output features (A's M), kdim: contraction length
     int f16;                             // 16-bit elements are fp16 (else bf16)
     int chunked;                         // bit 0: a0 and a1, bit 1: b see K (gradient: A's features) in 128-byte chunks
@@ -272,8 +272,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
         const int local = tile - te.y, n_e = te.w, per = te.x >> 16;   // balanced rows per tile
         // the features of a row block run fastest: the CTAs of a wave share the rows, and the expert's
         // weights stay in L2 from one row block to the next
-        int n = int(__umulhi(uint32_t(local), a.mt_inv));              // local / MT, or one less
-        n += (n + 1) * MT <= local ? 1 : 0;
+        const int n = mm_div(local, MT, a.mt_inv);
         t.m0 = (local - n * MT) * (128 * CG);
         t.nval = min(per, n_e - n * per);
         t.n0 = te.z + n * per;
@@ -687,8 +686,7 @@ int launch_grouped_mm(const MmProblem& p, cudaStream_t s) {
     a.rows = p.rows;
     a.f16 = p.f16;
     a.early = p.i8;
-    const uint32_t mt = uint32_t(a.mdim + (pair ? 255 : 127)) / (pair ? 256u : 128u);
-    a.mt_inv = mt > 1 ? uint32_t((uint64_t(1) << 32) / mt) : 0xffffffffu;
+    a.mt_inv = mm_inverse(uint32_t(a.mdim + (pair ? 255 : 127)) / (pair ? 256u : 128u));
     if (pair) {
         // Experts of some hundred rows or fewer on average: the small ones' tiles wait for memory beside the large
         // ones' (65,536 rows, Zipf over 352 experts, int8 gate/up: 1096 us against 1171; over 44 experts the weights

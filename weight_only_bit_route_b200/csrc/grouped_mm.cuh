@@ -37,6 +37,13 @@ struct MmSequence {
     }
 };
 
+// n / d for 0 <= n, with inv = mm_inverse(d): a division costs some hundred cycles, and every role would make one per tile
+__device__ __forceinline__ int mm_div(int n, int d, uint32_t inv) {
+    const int q = int(__umulhi(uint32_t(n), inv));                   // n / d, or one less
+    return q + ((q + 1) * d <= n ? 1 : 0);
+}
+inline uint32_t mm_inverse(uint32_t d) { return d > 1 ? uint32_t((uint64_t(1) << 32) / d) : 0xffffffffu; }
+
 // Position of expert e among the experts by rows, most first (n: rows of the E experts in shared memory, zeros up to
 // the next multiple of 4).
 __device__ __forceinline__ int mm_rank(const int* n, int E, int e) {
