@@ -172,6 +172,41 @@ def test_weight_gradients_of_many_rows(counts, K, N, dtype):
             assert ((got.double() - want).abs() <= product_bound(mag, b - a, want, got.dtype)).all(), (e, got.dtype)
 
 
+@pytest.mark.parametrize("E,n_experts,rows_of", [(44, 16, 1), (44, 16, 3), (44, 40, 1), (3, 3, 65), (5, 5, 66), (44, 9, 40)])
+def test_clusters_take_several_tiles(E, n_experts, rows_of):
+    """Long contractions over more tiles than clusters: a cluster joins tile after tile, most of whose epilogue warps
+    have nothing to send or to sum when an expert holds few rows."""
+    K, N = 2048, 1536
+    counts = [rows_of] * n_experts + [0] * (E - n_experts)
+    g = gen(28)
+    rows = sum(counts)
+    x, w = normal(g, rows, K), normal(g, E, N, K, std=0.1)
+    x8, gate, up, down = normal(g, rows, K), int8_bank(g, E, N, K), int8_bank(g, E, N, K), int8_bank(g, E, K, N)
+    off, rs = offsets_of(counts), torch.arange(rows, dtype=torch.int32, device="cuda")
+    ws = moe.workspace(rows, K, E, N, 1)
+    wt = w.transpose(1, 2).contiguous()
+    runs = [[moe.grouped_mm(x, w, off, ws), moe.grouped_mm_dgrad(x, wt, off, ws),
+             moe.grouped_swiglu(x8, off, rs, 1, gate, up, rows, ws), moe.grouped_down(x8[:, :N].contiguous(), off, rs, None, down, ws)]
+            for _ in range(5)]
+    assert moe.read_status(ws) == 0
+    for r in runs[1:]:
+        for a, b in zip(r, runs[0]):
+            assert torch.equal(a, b)
+    y, dx, h, d = runs[0]
+    q, s = codes_of(x8)
+    qd, sd = codes_of(x8[:, :N].contiguous())
+    for e, a, b in spans(counts)[:n_experts]:
+        xe, we = x[a:b].double(), w[e].double()
+        ref, mag = xe @ we.T, xe.abs() @ we.abs().T
+        for got in (y, dx):
+            assert ((got[a:b].double() - ref).abs() <= product_bound(mag, K, ref, torch.bfloat16)).all(), e
+        gg, uu = product8(q[a:b], s[a:b], gate, e), product8(q[a:b], s[a:b], up, e)
+        ref = gg * torch.sigmoid(gg) * uu
+        assert ((h[a:b].double() - ref).abs() <= ref.abs() * (2.0 ** -8 + (1 + gg.abs()) * 2.0 ** -20) + 1e-30).all(), e
+        ref = product8(qd[a:b], sd[a:b], down, e)
+        assert ((d[a:b].double() - ref).abs() <= ref.abs() * (2.0 ** -8 + 2.0 ** -20) + 1e-30).all(), e
+
+
 def test_no_rows_at_all():
     """Empty row tensors: nothing to multiply, a zero gradient, an accumulated one left as it was."""
     off, ws, K, N = offsets_of([0, 0]), moe.control_block(), 72, 136

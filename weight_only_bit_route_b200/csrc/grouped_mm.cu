@@ -30,6 +30,7 @@
 // Every wait is bounded (moe_set_wait_limit).  On expiry the kernel records MOE_ERR_TIMEOUT, stops issuing work,
 // waits (bounded) for its copies and MMAs in flight, frees its tensor memory and returns.
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 
 #include "grouped_mm.cuh"
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
     using C = MmCfg<I8, AMN, GU, NT, CG, SL, SPLIT>;
     constexpr int S = C::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ __align__(8) uint64_t full[S], empty[S], acc_full[2], acc_empty[2], drain, hold_bar, red_full, red_free;
+    __shared__ __align__(8) uint64_t full[S], empty[S], acc_full[2], acc_empty[2], drain, hold_bar, red_full, red_done, red_free;
     __shared__ uint32_t s_tmem;
     __shared__ uint32_t s_issued[2];                 // stages this CTA's two producers have issued
     __shared__ int s_wsum[MM_THREADS / 32], s_wt[MM_THREADS / 32], s_nact, s_total, s_hold;
@@ -170,7 +171,8 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
         asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(g_smem(&hold_bar)));
         if (SPLIT) {
             asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(g_smem(&red_full)));
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(g_smem(&red_free)), "r"((z - 1) * MM_EPI_WARPS));
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(g_smem(&red_done)), "r"(MM_EPI_WARPS));
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(g_smem(&red_free)), "r"(z));
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         s_ab.flag = 0;
@@ -473,6 +475,8 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
             uint16_t* dst = a.out + size_t(T.n0 + odd) * a.mdim + (m - odd);
             if constexpr (SPLIT) {
                 // Block b of 16 rows is summed by CTA b mod z: hand it the others' partial sums, then wait for theirs.
+                // A tile's partial sums go out once every CTA, this one among them, is through with the tile before
+                // (red_free): a warp with nothing to send or to sum can then neither be lapped nor run ahead.
                 if (ti > 0 && !g_wait_long(g_smem(&red_free), (ti - 1) & 1, &s_ab)) {
                     ok = false;
                     break;
@@ -557,7 +561,17 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
                 }
             }
             use.take(h, both);
-            if (SPLIT && ti + 1 < seq.count && lane < z && lane != int(krank)) g_arrive_remote(g_mapa(g_smem(&red_free), lane));
+            if (SPLIT && ti + 1 < seq.count) {
+                if (lane == 0) g_arrive(g_smem(&red_done));
+                __syncwarp();
+                if (warp == 4) {                                              // for the CTA's epilogue warps
+                    if (!g_wait_long(g_smem(&red_done), ti & 1, &s_ab)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane < z) g_arrive_remote(g_mapa(g_smem(&red_free), lane));
+                }
+            }
         }
         if (!ok) fail();
     }
@@ -612,7 +626,9 @@ static int mm_launch(const MmArgs& a, cudaStream_t s) {
 
 static int mm_mdim(const MmProblem& p) { return p.grad ? p.in_dim : p.out_dim; }
 // About how many (expert, row block) pairs there are with blocks of nt rows
-static int64_t mm_row_blocks(const MmProblem& p, int nt) { return std::max(std::min(p.E, p.rows), (p.rows + nt - 1) / nt); }
+static int64_t mm_row_blocks(const MmProblem& p, int nt) {
+    return std::max(int64_t(std::min(p.E, p.rows)), (int64_t(p.rows) + nt - 1) / nt);
+}
 
 // Tiles of 256 rows x 256 features on CTA pairs when the experts hold more than 64 rows on average (int8: 32, whose
 // MMAs take half the time) and half the pairs get a tile; else 64 rows x 128 features on single CTAs.  Measured (4096
@@ -625,16 +641,25 @@ static bool mm_pair(const MmProblem& p) {
 }
 // K slices per stage: two where the stage then still fits the ring four times
 static int mm_slices(const MmProblem& p) { return p.w1 ? 1 : 2; }
-// Few tiles leave SMs idle: then clusters of 2, 4 or 8 CTAs (gate/up: 4 at most) share each tile's K, as many as give
-// every SM a CTA, while each still has two stages of K (one expert, 4096 -> 1536: 8 rows 18 us without, 9 with; int8
-// gate/up of 61 rows 18 / 13).
+// Few tiles leave SMs idle: then clusters of 2, 4 or 8 CTAs (gate/up: 4 at most) share each tile's K, as many as
+// 148, 132 or 120 SMs hold at once, while each CTA still has two stages of K (one expert, 4096 -> 1536: 8 rows 18 us
+// without, 8 with; int8 gate/up of 61 rows 18 / 12).  Pairs of CTAs also turn two rounds of long tiles, the second at
+// most half full, into one and a half (two tokens over 16 experts of 4096 -> 1536, bf16: 43 us / 37; one expert of
+// 1000 rows 30 / 26; but clusters of 4 over several rounds lose: one token, int8 gate/up, 19 / 32, and so do short
+// tiles, 16 experts of 1536 -> 4096 in int8 19 / 26, and gate/up, 28 / 33).
 static int mm_split(const MmProblem& p, int* tiles) {
     const int kdim = p.grad ? p.out_dim : p.in_dim;
     const int64_t t = mm_row_blocks(p, 64) * ((mm_mdim(p) + 127) / 128);
     const int bk = (p.i8 ? 128 : 64) * mm_slices(p), ks = (kdim + bk - 1) / bk;
+    const int most[] = {148, 148, 132, 120};
     int z = 1;
-    const int most[] = {148, 148, 132, 120};         // SMs that clusters of 1, 2, 4 and 8 can fill at once
-    for (int i = 1; z < (p.w1 ? 4 : 8) && t * 2 * z <= most[i] && ks >= 4 * z && int64_t(2 * z - 1) * ((ks + 2 * z - 1) / (2 * z)) < ks; i++) z *= 2;
+    for (int i = 1; z < (p.w1 ? 4 : 8) && t * 2 * z <= most[i] && ks >= 4 * z &&
+                    int64_t(2 * z - 1) * ((ks + 2 * z - 1) / (2 * z)) < ks; i++)
+        z *= 2;
+    // (of the experts, rows that spread evenly reach E (1 - exp(-rows / E)))
+    const double reached = std::max(p.E * (1.0 - std::exp(-double(p.rows) / p.E)), double(p.rows) / 64);
+    const double likely = reached * ((mm_mdim(p) + 127) / 128);
+    if (!p.w1 && likely > 148 && likely <= 222 && ks >= 16) z = 2;
     *tiles = int(std::min<int64_t>(t, 1 << 20));
     return z;
 }
