@@ -316,7 +316,10 @@ int moe_grouped_w4a16_down(const void* h_perm, const int32_t* expert_offsets,
  *                          the sums are added to dw, which must be fp32
  * x, dx: [rows, in_dim]; y, dy: [rows, out_dim]; w, dw: [E, out_dim, in_dim];
  * all of one 16-bit type (f16 = 0: bf16, 1: IEEE fp16), dw also fp32
- * (dw_f32 = 1).  Sums are fp32, rounded once.  out_dim and in_dim are multiples
+ * (dw_f32 = 1).  Sums are fp32, rounded once to the output type; the tensor core's
+ * own sums are cut off rather than rounded, so it adds no more than 1024 terms
+ * (weight gradient: 512 rows) at a time, and those partial sums are added
+ * rounded to nearest.  out_dim and in_dim are multiples
  * of 8, E <= 1024, tensors 16-byte aligned and contiguous; rows is the row count
  * of the tensors.  Offsets that decrease or leave [0, rows] are clipped to it
  * and recorded as MOE_ERR_DEVICE_INDEX.  Results do not depend on the order in

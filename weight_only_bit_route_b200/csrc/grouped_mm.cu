@@ -23,6 +23,12 @@
 //              epilogue of a tile overlaps the next tile's products.
 // B's rows behind the tile's last are other experts' rows: their columns are computed and never stored.
 //
+// The tensor core's fp32 sums are cut off rather than rounded, an error that grows with the contraction.  So in 16 bits
+// only kMmChunk = 1024 terms are summed in tensor memory at a time, and the epilogue adds those partial sums in fp32
+// registers, rounded to nearest.  Of the bf16 results over K = 4096, 0.7 in a thousand then differ from those of plain
+// fp32 sums; 2.3 with one sum, 0.5 with chunks of 512.  Time in a loop, one sum / 1024 / 512 (44 experts, 65,536 rows):
+// K = 4096 724 / 727 / 750 us, K = 1536 728 / 739 / 770; 8 tokens over 352 experts 119.0 / 119.5 / 119.9.
+//
 // Bound by the weight stream up to some hundred rows per expert (352 experts of 4096 x 1536: 8 tokens 117 us in bf16,
 // 114 us for int8 gate and up, 6.3 and 6.5 TB/s; 2048 tokens 682 us, 6.8 TB/s), by the tensor pipe and the power cap
 // above (65,536 rows over 44 experts: 1360 TFLOP/s in a burst, 1150 sustained at 1.1 to 1.2 GHz, the pipe 83 % active).
@@ -41,6 +47,8 @@ namespace moe {
 constexpr int MM_THREADS = 384;
 constexpr int MM_EPI_WARPS = 8;
 constexpr int MM_BOXES = 4;
+// 16 bits: terms summed in tensor memory at a time (integer sums are exact)
+constexpr int kMmChunk = 1024;
 
 // Tile shape of one instantiation.  NT: rows per tile; CG: CTAs per tile; SL: 128-byte slices of K per stage; SPLIT:
 // a cluster shares a tile's K.
@@ -64,6 +72,8 @@ struct MmCfg {
     static constexpr int kHalfCols = kMat * kHalfRows;
     static constexpr int kTmemCols = 2 * kHalfCols;
     static constexpr int kTmem = kTmemCols <= 32 ? 32 : (kTmemCols <= 64 ? 64 : (kTmemCols <= 128 ? 128 : (kTmemCols <= 256 ? 256 : 512)));
+    static constexpr int kChunk = I8 ? 1 << 30 : kMmChunk / kBK;  // stages summed in tensor memory at a time
+    static constexpr int kSums = I8 ? 1 : (NT + 31) / 32 * 16;    // of one epilogue thread
     static constexpr int kStep = 16 * CG;                         // a tile's N is a multiple of this
     static_assert(kAccCols <= 512 && NT % kStep == 0 && kStages >= 2, "tile shape");
     static_assert(!SPLIT || (CG == 1 && NT <= 64), "split K: the partial sums fit");
@@ -368,18 +378,23 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
             const uint32_t idesc = I8 ? g_idesc_s8(T.bn, 128 * CG)
                                       : (g_idesc(T.bn, a.f16 != 0, 128 * CG) | (AMN ? G_IDESC_A_MN : 0u));
             const bool both = T.bn > C::kHalfRows;
-            const uint32_t h = both ? 0 : acc.next;
-            const uint32_t d = tmem + h * C::kHalfCols, up = both ? NT : C::kHalfRows;
+            uint32_t h = 0, d = 0;
+            const uint32_t up = both ? NT : C::kHalfRows;
             const int half = T.bn / CG;
             const uint32_t slice = (half <= 16 ? 16u : half <= 32 ? 32u : half <= 64 ? 64u : 128u) * 128u;
-            if ((acc.uses(h) && !g_wait_long(g_smem(&acc_empty[h]), (acc.uses(h) - 1) & 1, &s_ab)) ||
-                (both && acc.u1 && !g_wait_long(g_smem(&acc_empty[1]), (acc.u1 - 1) & 1, &s_ab))) {
-                ok = false;
-                break;
-            }
-            acc.take(h, both);
-            g_fence_after();
             for (int ks = ks0; ks < ks1; ks++, it++) {
+                const int kc = (ks - ks0) % C::kChunk;
+                if (kc == 0) {
+                    h = both ? 0 : acc.next;
+                    d = tmem + h * C::kHalfCols;
+                    if ((acc.uses(h) && !g_wait_long(g_smem(&acc_empty[h]), (acc.uses(h) - 1) & 1, &s_ab)) ||
+                        (both && acc.u1 && !g_wait_long(g_smem(&acc_empty[1]), (acc.u1 - 1) & 1, &s_ab))) {
+                        ok = false;
+                        break;
+                    }
+                    acc.take(h, both);
+                    g_fence_after();
+                }
                 const int s = it % S;
                 if (!g_wait_long(g_smem(&full[s]), (it / S) & 1, &s_ab)) {
                     ok = false;
@@ -393,7 +408,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
                     for (int k = 0; k < 4 * SL; k++) {
                         if (k >= steps) break;                     // K ends here
                         const uint64_t bd = g_desc(sb + (k / 4) * slice + (k % 4) * 32);
-                        const uint32_t add = (k > 0 || ks > ks0) ? 1u : 0u;
+                        const uint32_t add = (k > 0 || kc > 0) ? 1u : 0u;
 #pragma unroll
                         for (int m = 0; m < C::kMat; m++) {
                             const uint32_t am = sa + m * C::kABytes;
@@ -404,7 +419,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
                         }
                     }
                     g_commit_cg<CG>(g_smem(&empty[s]));
-                    if (ks == ks1 - 1) {
+                    if (kc == C::kChunk - 1 || ks == ks1 - 1) {
                         g_commit_cg<CG>(g_smem(&acc_full[h]));
                         if (both) g_commit_cg<CG>(g_smem(&acc_full[1]));
                     }
@@ -453,6 +468,14 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
             }
             return p;
         };
+        auto release = [&](uint32_t half) {                                   // this warp has read the accumulator
+            g_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                const uint32_t bar = g_smem(&acc_empty[half]);
+                if (CG == 2) g_arrive_remote_relaxed(g_mapa(bar, 0)); else g_arrive(bar);
+            }
+        };
         Pre next;
         if (seq.count > 0) next = fetch(0);
         for (int ti = 0; ti < seq.count && !g_aborted(&s_ab); ti++) {
@@ -462,6 +485,33 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
             const bool mine = m < a.mdim;
             const float w0 = cur.w0, w1 = cur.w1;
             const float (&rs)[kScaleRegs] = cur.rs;
+            // 16 bits: the partial sums of all chunks of K but the last
+            float sum[C::kSums];
+#pragma unroll
+            for (int j = 0; j < C::kSums; j++) sum[j] = 0.f;
+            if constexpr (!I8) {
+                for (int left = ks1 - ks0; left > C::kChunk; left -= C::kChunk) {
+                    const uint32_t part = use.next;
+                    if (!g_wait_long(g_smem(&acc_full[part]), use.uses(part) & 1, &s_ab)) {
+                        ok = false;
+                        break;
+                    }
+                    g_fence_after();
+#pragma unroll
+                    for (int i = 0; i < C::kSums / 16; i++) {
+                        const int c = (2 * i + hsel) * 16;
+                        if (c >= T.nval) break;
+                        uint32_t v[16];
+                        g_ld16(tmem + lane_addr + part * C::kHalfCols + c, v);
+                        g_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; j++) sum[16 * i + j] += __uint_as_float(v[j]);
+                    }
+                    release(part);
+                    use.take(part, false);
+                }
+                if (!ok) break;
+            }
             const bool both = T.bn > C::kHalfRows;
             const uint32_t h = both ? 0 : use.next;
             if (!g_wait_long(g_smem(&acc_full[h]), use.uses(h) & 1, &s_ab) ||
@@ -472,6 +522,15 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
             g_fence_after();
             if (ti + 1 < seq.count) next = fetch(ti + 1);
             const uint32_t acc = tmem + lane_addr + h * C::kHalfCols, up = both ? NT : C::kHalfRows;
+            // block i of this warp's, 16 columns, as bits (i is a constant after unrolling)
+            auto block = [&](int i, uint32_t (&v)[16], uint32_t (&u)[16]) {
+                g_ld16(acc + (2 * i + hsel) * 16, v);
+                if constexpr (GU) g_ld16(acc + up + (2 * i + hsel) * 16, u);
+                g_ld_wait();
+                if constexpr (!I8)
+#pragma unroll
+                    for (int j = 0; j < 16; j++) v[j] = __float_as_uint(sum[16 * i + j] + __uint_as_float(v[j]));
+            };
             uint16_t* dst = a.out + size_t(T.n0 + odd) * a.mdim + (m - odd);
             if constexpr (SPLIT) {
                 // Block b of 16 rows is summed by CTA b mod z: hand it the others' partial sums, then wait for theirs.
@@ -485,16 +544,17 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
                 constexpr uint32_t kPart = C::kMat * 8192;                                        // a block's partial sums
                 const uint32_t per = uint32_t(C::kBlocks / z + (C::kBlocks < z)) * kPart;         // room for one CTA's
                 if (warp == 4 && lane == 0) g_expect(g_smem(&red_full), uint32_t(nown * (z - 1)) * kPart);
-                for (int b = hsel; b < nblk; b += 2) {
+#pragma unroll
+                for (int i = 0; i < (NT + 31) / 32; i++) {
+                    const int b = 2 * i + hsel;
+                    if (b >= nblk) break;
                     const uint32_t own = uint32_t(b) & (z - 1);
                     if (own == krank) continue;
                     const uint32_t to = g_mapa(g_smem(red), own) + (krank < own ? krank : krank - 1) * per +
                                         uint32_t(b / z) * kPart + uint32_t(q * 32 + lane) * 16;
                     const uint32_t bar = g_mapa(g_smem(&red_full), own);
                     uint32_t v[16], u[16];
-                    g_ld16(acc + b * 16, v);
-                    if constexpr (GU) g_ld16(acc + up + b * 16, u);
-                    g_ld_wait();
+                    block(i, v, u);
 #pragma unroll
                     for (int j = 0; j < 4; j++) {
                         g_st_async4(to + j * 2048, v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3], bar);
@@ -512,9 +572,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
                 if (c >= T.nval) break;
                 if (SPLIT && (uint32_t(c / 16) & (z - 1)) != krank) continue;
                 uint32_t v[16], u[16];
-                g_ld16(acc + c, v);
-                if constexpr (GU) g_ld16(acc + up + c, u);
-                g_ld_wait();
+                block(i, v, u);
                 if constexpr (SPLIT) {
                     mm_join<I8>(v, red + (c / 16 / z) * (C::kMat * 8192), C::kMat * 8192 * (C::kBlocks / z + (C::kBlocks < z)),
                                 z, krank, q * 32 + lane);
@@ -552,14 +610,8 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
                     if (mine && c + j + odd < T.nval) *reinterpret_cast<uint32_t*>(row + size_t(j) * a.mdim) = p;
                 }
             }
-            g_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                for (uint32_t i = h; i <= (both ? 1u : h); i++) {
-                    const uint32_t bar = g_smem(&acc_empty[i]);
-                    if (CG == 2) g_arrive_remote_relaxed(g_mapa(bar, 0)); else g_arrive(bar);
-                }
-            }
+            release(h);
+            if (both) release(1);
             use.take(h, both);
             if (SPLIT && ti + 1 < seq.count) {
                 if (lane == 0) g_arrive(g_smem(&red_done));
