@@ -120,8 +120,9 @@ int run_int8(const GemvProblem& p, bool gateup, int rows, int ntok, void* prep, 
     if (two) {
         float* tok_scales = reinterpret_cast<float*>(base + align256(size_t(rows) * 4));
         int8_t* tok_codes = codes + align256(size_t(rows) * p.in_dim);
+        // no status here: a token that no row refers to is nobody's error (the copy records those of the rows)
         MOE_TRY(launch_quant_int8(p.act, p.act_f16 != 0, ntok, p.in_dim, nullptr, 1, ntok, nullptr, nullptr, tok_codes,
-                                  tok_scales, p.status, s));
+                                  tok_scales, nullptr, s));
         MOE_TRY(launch_gather_int8(tok_codes, tok_scales, rows, p.in_dim, p.row_slot, p.top_k, ntok, p.offsets + p.E, codes,
                                    scales, p.status, s));
     } else {

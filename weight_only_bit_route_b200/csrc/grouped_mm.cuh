@@ -86,7 +86,8 @@ int launch_grouped_wgrad(const WgradProblem& p, cudaStream_t s);
 int launch_quant_int8(const void* x, bool f16, int64_t rows, int64_t cols, const int32_t* row_slot, int top_k,
                       int64_t nsrc, const float* row_w, const int32_t* nrows, int8_t* codes, float* scales,
                       int32_t* status, cudaStream_t s);
-// Rows of codes and their scales by slot, as above, from the nsrc rows src, src_scales.
+// Rows of codes and their scales by slot, as above, from the nsrc rows src, src_scales.  A row of scale NaN is recorded
+// as MOE_ERR_NONFINITE.
 int launch_gather_int8(const int8_t* src, const float* src_scales, int rows, int cols, const int32_t* row_slot, int top_k,
                        int nsrc, const int32_t* nrows, int8_t* codes, float* scales, int32_t* status, cudaStream_t s);
 

@@ -156,8 +156,10 @@ __global__ void __launch_bounds__(Q8_THREADS) gather_int8_kernel(const int8_t* _
     if (row >= *nrows) return;
     const long long t = q8_source(row_slot[row], top_k, nsrc);
     if (threadIdx.x == 0) {
-        scales[row] = t < 0 ? 0.f : src_scales[t];
+        const float scale = t < 0 ? 0.f : src_scales[t];
+        scales[row] = scale;
         if (t < 0) set_status(status, MOE_ERR_DEVICE_INDEX);
+        else if (isnan(scale)) set_status(status, MOE_ERR_NONFINITE);     // (of a row, not of a token that none refers to)
     }
     const uint4* p = reinterpret_cast<const uint4*>(src + (t < 0 ? 0 : t) * cols);
     uint4* d = reinterpret_cast<uint4*>(codes + size_t(row) * cols);
