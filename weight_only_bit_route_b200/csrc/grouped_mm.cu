@@ -27,7 +27,7 @@
 // only kMmChunk = 1024 terms are summed in tensor memory at a time, and the epilogue adds those partial sums in fp32
 // registers, rounded to nearest.  Of the bf16 results over K = 4096, 0.7 in a thousand then differ from those of plain
 // fp32 sums; 2.3 with one sum, 0.5 with chunks of 512.  Time in a loop, one sum / 1024 / 512 (44 experts, 65,536 rows):
-// K = 4096 724 / 727 / 750 us, K = 1536 728 / 739 / 770; 8 tokens over 352 experts 119.0 / 119.5 / 119.9.
+// K = 4096 723 / 727 / 740 us, K = 1536 722 / 736 / 757 (chunks of 1536: 730); 8 tokens over 352 experts 118.7 / 119.4 / 119.8.
 //
 // Bound by the weight stream up to some hundred rows per expert (352 experts of 4096 x 1536: 8 tokens 117 us in bf16,
 // 114 us for int8 gate and up, 6.3 and 6.5 TB/s; 2048 tokens 682 us, 6.8 TB/s), by the tensor pipe and the power cap
@@ -378,53 +378,51 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
             const uint32_t idesc = I8 ? g_idesc_s8(T.bn, 128 * CG)
                                       : (g_idesc(T.bn, a.f16 != 0, 128 * CG) | (AMN ? G_IDESC_A_MN : 0u));
             const bool both = T.bn > C::kHalfRows;
-            uint32_t h = 0, d = 0;
             const uint32_t up = both ? NT : C::kHalfRows;
             const int half = T.bn / CG;
             const uint32_t slice = (half <= 16 ? 16u : half <= 32 ? 32u : half <= 64 ? 64u : 128u) * 128u;
-            for (int ks = ks0; ks < ks1; ks++, it++) {
-                const int kc = (ks - ks0) % C::kChunk;
-                if (kc == 0) {
-                    h = both ? 0 : acc.next;
-                    d = tmem + h * C::kHalfCols;
-                    if ((acc.uses(h) && !g_wait_long(g_smem(&acc_empty[h]), (acc.uses(h) - 1) & 1, &s_ab)) ||
-                        (both && acc.u1 && !g_wait_long(g_smem(&acc_empty[1]), (acc.u1 - 1) & 1, &s_ab))) {
-                        ok = false;
-                        break;
-                    }
-                    acc.take(h, both);
-                    g_fence_after();
-                }
-                const int s = it % S;
-                if (!g_wait_long(g_smem(&full[s]), (it / S) & 1, &s_ab)) {
+            for (int kc = ks0; kc < ks1 && ok; kc += C::kChunk) {
+                const int kend = min(ks1, kc + C::kChunk);
+                const uint32_t h = both ? 0 : acc.next, d = tmem + h * C::kHalfCols;
+                if ((acc.uses(h) && !g_wait_long(g_smem(&acc_empty[h]), (acc.uses(h) - 1) & 1, &s_ab)) ||
+                    (both && acc.u1 && !g_wait_long(g_smem(&acc_empty[1]), (acc.u1 - 1) & 1, &s_ab))) {
                     ok = false;
                     break;
                 }
+                acc.take(h, both);
                 g_fence_after();
-                const uint32_t sa = g_smem(ring + s * C::kStage), sb = sa + C::kMat * C::kABytes;
-                const int steps = min(4 * SL, (a.kdim - ks * C::kBK + C::kMmaK - 1) / C::kMmaK);
-                if (g_elect()) {
+                for (int ks = kc; ks < kend; ks++, it++) {
+                    const int s = it % S;
+                    if (!g_wait_long(g_smem(&full[s]), (it / S) & 1, &s_ab)) {
+                        ok = false;
+                        break;
+                    }
+                    g_fence_after();
+                    const uint32_t sa = g_smem(ring + s * C::kStage), sb = sa + C::kMat * C::kABytes;
+                    const int steps = min(4 * SL, (a.kdim - ks * C::kBK + C::kMmaK - 1) / C::kMmaK);
+                    if (g_elect()) {
 #pragma unroll
-                    for (int k = 0; k < 4 * SL; k++) {
-                        if (k >= steps) break;                     // K ends here
-                        const uint64_t bd = g_desc(sb + (k / 4) * slice + (k % 4) * 32);
-                        const uint32_t add = (k > 0 || kc > 0) ? 1u : 0u;
+                        for (int k = 0; k < 4 * SL; k++) {
+                            if (k >= steps) break;                 // K ends here
+                            const uint64_t bd = g_desc(sb + (k / 4) * slice + (k % 4) * 32);
+                            const uint32_t add = (k > 0 || ks > kc) ? 1u : 0u;
 #pragma unroll
-                        for (int m = 0; m < C::kMat; m++) {
-                            const uint32_t am = sa + m * C::kABytes;
-                            const uint64_t ad = AMN ? g_desc_mn(am + k * 2048, SL * 8192)
-                                                    : g_desc(am + (k / 4) * 16384 + (k % 4) * 32);
-                            if (I8) g_mma_s8<CG>(d + m * up, ad, bd, idesc, add);
-                            else g_mma_f16<CG>(d + m * up, ad, bd, idesc, add);
+                            for (int m = 0; m < C::kMat; m++) {
+                                const uint32_t am = sa + m * C::kABytes;
+                                const uint64_t ad = AMN ? g_desc_mn(am + k * 2048, SL * 8192)
+                                                        : g_desc(am + (k / 4) * 16384 + (k % 4) * 32);
+                                if (I8) g_mma_s8<CG>(d + m * up, ad, bd, idesc, add);
+                                else g_mma_f16<CG>(d + m * up, ad, bd, idesc, add);
+                            }
+                        }
+                        g_commit_cg<CG>(g_smem(&empty[s]));
+                        if (ks == kend - 1) {
+                            g_commit_cg<CG>(g_smem(&acc_full[h]));
+                            if (both) g_commit_cg<CG>(g_smem(&acc_full[1]));
                         }
                     }
-                    g_commit_cg<CG>(g_smem(&empty[s]));
-                    if (kc == C::kChunk - 1 || ks == ks1 - 1) {
-                        g_commit_cg<CG>(g_smem(&acc_full[h]));
-                        if (both) g_commit_cg<CG>(g_smem(&acc_full[1]));
-                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
         }
         if (!ok) fail();
