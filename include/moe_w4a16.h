@@ -321,8 +321,9 @@ int moe_grouped_w4a16_down(const void* h_perm, const int32_t* expert_offsets,
  * (weight gradient: 512 rows) at a time, and those partial sums are added
  * rounded to nearest.  out_dim and in_dim are multiples
  * of 8, E <= 1024, tensors 16-byte aligned and contiguous; rows is the row count
- * of the tensors.  Offsets that decrease or leave [0, rows] are clipped to it
- * and recorded as MOE_ERR_DEVICE_INDEX.  Results do not depend on the order in
+ * of the tensors.  Offsets that decrease or leave [0, rows] are recorded as
+ * MOE_ERR_DEVICE_INDEX; each then counts as the largest up to it, clipped to
+ * [0, rows], so that no two experts share a row.  Results do not depend on the order in
  * which tiles run; accumulate takes magnitudes below 2^-126 for zero.  Outputs
  * must not overlap inputs.  ws: at least 1024 bytes (the control block), zero-filled
  * once; it holds no intermediate results. */

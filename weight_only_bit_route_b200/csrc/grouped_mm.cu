@@ -207,19 +207,27 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
     if constexpr (kSort) {
         int* rows_of = reinterpret_cast<int*>(ring);                 // scratch until the copies start
         const int pad = (a.E + 3) & ~3;
+        bool good = true;
         for (int e = tid; e < pad; e += MM_THREADS) {
             int base = 0, n = 0;
-            if (e < a.E) mm_expert_rows(a.offsets, e, a.rows, a.status, base, n);
+            if (e < a.E) good &= mm_expert_rows(a.offsets, e, a.rows, base, n);
             rows_of[e] = n;
         }
-        __syncthreads();
+        const bool clip = __syncthreads_or(!good);
+        if (clip) {
+            if (tid == 0) set_status(a.status, MOE_ERR_DEVICE_INDEX);
+            for (int e = tid; e < a.E; e += MM_THREADS) rows_of[e] = mm_clipped_rows(a.offsets, e, a.rows).y;
+            __syncthreads();
+        }
         for (int e = tid; e < a.E; e += MM_THREADS)
-            tbl[mm_rank(rows_of, a.E, e)] = make_int4(e, 0, min(max(a.offsets[e], 0), a.rows), rows_of[e]);
+            tbl[mm_rank(rows_of, a.E, e)] =
+                make_int4(e, 0, clip ? mm_clipped_rows(a.offsets, e, a.rows).x : a.offsets[e], rows_of[e]);
         g_fence_proxy_async();                                       // before the copies write the scratch
         __syncthreads();
     }
     {
         int ex[PER], eb[PER], ne[PER], nt[PER], local = 0, ltiles = 0;
+        bool good = true;
 #pragma unroll
         for (int i = 0; i < PER; i++) {
             const int e = tid * PER + i;
@@ -233,9 +241,22 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
                     eb[i] = te.z;
                     ne[i] = te.w;
                 } else {
-                    mm_expert_rows(a.offsets, e, a.rows, a.status, eb[i], ne[i]);
+                    good &= mm_expert_rows(a.offsets, e, a.rows, eb[i], ne[i]);
                 }
             }
+        }
+        if (!kSort && __syncthreads_or(!good)) {
+            if (tid == 0) set_status(a.status, MOE_ERR_DEVICE_INDEX);
+#pragma unroll
+            for (int i = 0; i < PER; i++) {
+                if (ex[i] >= a.E) continue;
+                const int2 r = mm_clipped_rows(a.offsets, ex[i], a.rows);
+                eb[i] = r.x;
+                ne[i] = r.y;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < PER; i++) {
             nt[i] = ((ne[i] + NT - 1) / NT) * MT;
             local += ne[i] > 0;
             ltiles += nt[i];

@@ -7,15 +7,20 @@ namespace moe {
 
 constexpr int kMmMaxRows = INT32_MAX - 1024;     // a tile's row numbers stay 32-bit
 
-// The rows of expert e: [base, base + n).  Offsets outside [0, rows] or decreasing are clipped and recorded, so
-// that no index derived from them leaves the rows.
-__device__ __forceinline__ void mm_expert_rows(const int32_t* offsets, int e, int rows, int32_t* status, int& base,
-                                               int& n) {
-    const int o0 = offsets[e], o1 = offsets[e + 1];
-    base = min(max(o0, 0), rows);
-    const int end = min(max(o1, base), rows);
+// The rows of expert e: [base, base + n).  False if its offsets leave [0, rows] or decrease: then every expert's rows are
+// those of mm_clipped_rows.
+__device__ __forceinline__ bool mm_expert_rows(const int32_t* offsets, int e, int rows, int& base, int& n) {
+    base = offsets[e];
+    const int end = offsets[e + 1];
     n = end - base;
-    if (base != o0 || end != o1) set_status(status, MOE_ERR_DEVICE_INDEX);
+    return base >= 0 && end >= base && end <= rows;
+}
+// The same with every offset raised to the largest before it and clipped to [0, rows]: no index derived from them leaves
+// the rows, and no two experts share one (the tiles of all of them then stay within 32 bits, and none is written twice).
+__device__ __forceinline__ int2 mm_clipped_rows(const int32_t* offsets, int e, int rows) {
+    int base = 0;
+    for (int i = 0; i <= e; i++) base = max(base, min(offsets[i], rows));
+    return make_int2(base, max(base, min(offsets[e + 1], rows)) - base);
 }
 
 // The tiles of worker p of P, as a sequence: tile p of each round of P, in snake order (every second round runs

@@ -124,16 +124,27 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
     {
         int* rows_of = reinterpret_cast<int*>(ring);                 // scratch until the copies start
         const int pad = (a.E + 3) & ~3;
+        bool good = true;
         for (int e = tid; e < pad; e += WG_THREADS) {
             int base = 0, n = 0;
-            if (e < a.E) mm_expert_rows(a.offsets, e, a.rows, a.status, base, n);
+            if (e < a.E) good &= mm_expert_rows(a.offsets, e, a.rows, base, n);
             if (kSort) rows_of[e] = n;
             else if (e < a.E) span[e] = make_int4(e, base, n, 0);
         }
-        if (kSort) {
+        const bool clip = __syncthreads_or(!good);
+        if (clip) {
+            if (tid == 0) set_status(a.status, MOE_ERR_DEVICE_INDEX);
+            for (int e = tid; e < a.E; e += WG_THREADS) {
+                const int2 r = mm_clipped_rows(a.offsets, e, a.rows);
+                if (kSort) rows_of[e] = r.y;
+                else span[e] = make_int4(e, r.x, r.y, 0);
+            }
             __syncthreads();
+        }
+        if (kSort) {
             for (int e = tid; e < a.E; e += WG_THREADS)
-                span[mm_rank(rows_of, a.E, e)] = make_int4(e, min(max(a.offsets[e], 0), a.rows), rows_of[e], 0);
+                span[mm_rank(rows_of, a.E, e)] =
+                    make_int4(e, clip ? mm_clipped_rows(a.offsets, e, a.rows).x : a.offsets[e], rows_of[e], 0);
             g_fence_proxy_async();                                   // before the copies write the scratch
         }
     }
