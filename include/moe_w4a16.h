@@ -301,8 +301,10 @@ int moe_grouped_w4a16_down(const void* h_perm, const int32_t* expert_offsets,
  * row row_slot[r] / top_k of x; a row that holds an infinity or a NaN records
  * MOE_ERR_NONFINITE and its outputs are NaN), each product is
  *     float(sum q[r,k] w[e,n,k]) * (row scale * channel scale)
- * with an exact 32-bit sum, and the rest is as above.  The workspace sizes
- * above are enough. */
+ * with an exact 32-bit sum, and the rest is as above.  Rows outside
+ * [expert_offsets[0], expert_offsets[E]) are neither read nor written; offsets
+ * that decrease or leave the rows count as under moe_grouped_mm below, with
+ * expert_offsets[E] as the rows' end.  The workspace sizes above are enough. */
 
 /* Products grouped by expert in 16 bits, for experts that are not quantised,
  * and their gradients (the pages describe the experts' products, The shape;

@@ -54,7 +54,6 @@ def test_bad_offsets_count_as_the_clipped_ones(kind, E, rows, K, N):
 
 @pytest.mark.parametrize("E,rows", [(4, 24), (4, 1000), (64, 5000)])
 def test_bad_offsets_of_the_8_bit_experts(E, rows):
-    """Rows behind the last offset hold no codes: here the last offset is the rows' end."""
     H, F = 512, 256
     g = gen(34)
     x = normal(g, rows, H)
@@ -66,3 +65,41 @@ def test_bad_offsets_of_the_8_bit_experts(E, rows):
          for o in (_clipped(bad, rows), bad)]
     assert moe.read_status(ws) == ERR_INDEX
     assert torch.equal(*h)
+
+
+@pytest.mark.parametrize("E,T,k,H,F", [(3, 20, 2, 512, 256), (16, 1100, 8, 2048, 128)])     # (the second copies the codes)
+def test_rows_of_no_expert_in_8_bits(E, T, k, H, F):
+    """Rows in front of the first expert and behind the last: their slots are not looked at, their values are nobody's
+    error, and the outputs' rows keep what they held."""
+    g = gen(35)
+    rows, first, last = T * k, 5, T * k - 9
+    x = normal(g, T, H)
+    gate, up, down = int8_bank(g, E, F, H), int8_bank(g, E, F, H), int8_bank(g, E, H, F)
+    off = torch.tensor([first + (last - first) * e // E for e in range(E + 1)], dtype=torch.int32, device="cuda")
+    rs = torch.arange(rows, dtype=torch.int32, device="cuda")
+    rs[:first], rs[last:] = -5, 2 ** 31 - 1
+    ws = moe.workspace(T, H, E, F, min(k, E))
+    h = torch.full((rows, F), 7.0, dtype=torch.bfloat16, device="cuda")
+    moe.grouped_swiglu(x, off, rs, k, gate, up, rows, ws, out=h)
+    assert moe.read_status(ws) == 0
+    assert (h[:first] == 7.0).all() and (h[last:] == 7.0).all()
+    h[:first], h[last:] = float("nan"), float("inf")
+    y = torch.full((rows, H), 7.0, dtype=torch.bfloat16, device="cuda")
+    moe.grouped_down(h, off, rs, torch.rand(rows, generator=g, device="cuda"), down, ws, out=y)
+    assert moe.read_status(ws) == 0
+    assert (y[:first] == 7.0).all() and (y[last:] == 7.0).all() and torch.isfinite(y).all()
+
+
+def test_rows_behind_a_falling_last_offset_in_8_bits():
+    """The last offset below the others: rows from it on have no codes, and none is multiplied."""
+    E, T, H, F = 3, 40, 512, 256
+    g = gen(36)
+    x, gate, up = normal(g, T, H), int8_bank(g, E, F, H), int8_bank(g, E, F, H)
+    rs = torch.arange(T, dtype=torch.int32, device="cuda")
+    ws = moe.workspace(T, H, E, F, 1)
+    h = []
+    for offsets in ([0, 10, 12, 12], [0, 10, 30, 12]):
+        h.append(torch.full((T, F), 7.0, dtype=torch.bfloat16, device="cuda"))
+        moe.grouped_swiglu(x, torch.tensor(offsets, dtype=torch.int32, device="cuda"), rs, 1, gate, up, T, ws, out=h[-1])
+    assert moe.read_status(ws) == ERR_INDEX
+    assert torch.equal(*h) and (h[1][12:] == 7.0).all()

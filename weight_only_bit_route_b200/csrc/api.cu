@@ -121,15 +121,15 @@ int run_int8(const GemvProblem& p, bool gateup, int rows, int ntok, void* prep, 
         float* tok_scales = reinterpret_cast<float*>(base + align256(size_t(rows) * 4));
         int8_t* tok_codes = codes + align256(size_t(rows) * p.in_dim);
         // no status here: a token that no row refers to is nobody's error (the copy records those of the rows)
-        MOE_TRY(launch_quant_int8(p.act, p.act_f16 != 0, ntok, p.in_dim, nullptr, 1, ntok, nullptr, nullptr, tok_codes,
+        MOE_TRY(launch_quant_int8(p.act, p.act_f16 != 0, ntok, p.in_dim, nullptr, 1, ntok, nullptr, nullptr, 0, tok_codes,
                                   tok_scales, nullptr, s));
-        MOE_TRY(launch_gather_int8(tok_codes, tok_scales, rows, p.in_dim, p.row_slot, p.top_k, ntok, p.offsets + p.E, codes,
+        MOE_TRY(launch_gather_int8(tok_codes, tok_scales, rows, p.in_dim, p.row_slot, p.top_k, ntok, p.offsets, p.E, codes,
                                    scales, p.status, s));
     } else {
         // down: the routing weight goes into the row's scale
         const float* row_w = gateup ? nullptr : p.topk_w;
         MOE_TRY(launch_quant_int8(p.act, p.act_f16 != 0, rows, p.in_dim, gateup || row_w ? p.row_slot : nullptr, p.top_k,
-                                  ntok, row_w, p.offsets + p.E, codes, scales, p.status, s));
+                                  ntok, row_w, p.offsets, p.E, codes, scales, p.status, s));
     }
     MmProblem m{};
     m.act = codes; m.act_scale = scales;
@@ -711,7 +711,7 @@ int moe_quantize_int8(const void* x, int64_t rows, int64_t cols, int f16, int8_t
     if (cols % 16 || rows > INT32_MAX) return MOE_ERR_UNSUPPORTED;
     if (rows == 0 || cols == 0) return MOE_OK;
     if (!x || !codes || !scales || !al16(x) || !al16(codes)) return MOE_ERR_INVALID_ARG;
-    return launch_quant_int8(x, f16 != 0, rows, cols, nullptr, 1, rows, nullptr, nullptr, codes, scales, nullptr, cs(stream));
+    return launch_quant_int8(x, f16 != 0, rows, cols, nullptr, 1, rows, nullptr, nullptr, 0, codes, scales, nullptr, cs(stream));
 }
 
 int moe_quantize_nvfp4_act(const void* x, int64_t rows, int64_t cols, const float* g, uint8_t* packed,

@@ -204,24 +204,26 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
     int4* tbl = reinterpret_cast<int4*>(red + C::kRedBytes);        // active experts: {expert | rows per tile << 16, first tile, first row, rows}
     constexpr bool kSort = CG == 2;                  // large batches: the experts' tiles from the most rows to the fewest
     constexpr int PER = (kMaxE + MM_THREADS - 1) / MM_THREADS;
+    // (8 bits: rows from offsets[E] on have no codes)
+    const int rows = I8 ? min(a.rows, max(a.offsets[a.E], 0)) : a.rows;
     if constexpr (kSort) {
         int* rows_of = reinterpret_cast<int*>(ring);                 // scratch until the copies start
         const int pad = (a.E + 3) & ~3;
         bool good = true;
         for (int e = tid; e < pad; e += MM_THREADS) {
             int base = 0, n = 0;
-            if (e < a.E) good &= mm_expert_rows(a.offsets, e, a.rows, base, n);
+            if (e < a.E) good &= mm_expert_rows(a.offsets, e, rows, base, n);
             rows_of[e] = n;
         }
         const bool clip = __syncthreads_or(!good);
         if (clip) {
             if (tid == 0) set_status(a.status, MOE_ERR_DEVICE_INDEX);
-            for (int e = tid; e < a.E; e += MM_THREADS) rows_of[e] = mm_clipped_rows(a.offsets, e, a.rows).y;
+            for (int e = tid; e < a.E; e += MM_THREADS) rows_of[e] = mm_clipped_rows(a.offsets, e, rows).y;
             __syncthreads();
         }
         for (int e = tid; e < a.E; e += MM_THREADS)
             tbl[mm_rank(rows_of, a.E, e)] =
-                make_int4(e, 0, clip ? mm_clipped_rows(a.offsets, e, a.rows).x : a.offsets[e], rows_of[e]);
+                make_int4(e, 0, clip ? mm_clipped_rows(a.offsets, e, rows).x : a.offsets[e], rows_of[e]);
         g_fence_proxy_async();                                       // before the copies write the scratch
         __syncthreads();
     }
@@ -241,7 +243,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
                     eb[i] = te.z;
                     ne[i] = te.w;
                 } else {
-                    good &= mm_expert_rows(a.offsets, e, a.rows, eb[i], ne[i]);
+                    good &= mm_expert_rows(a.offsets, e, rows, eb[i], ne[i]);
                 }
             }
         }
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(MM_THREADS, 1) mm_kernel(const __grid_constant
 #pragma unroll
             for (int i = 0; i < PER; i++) {
                 if (ex[i] >= a.E) continue;
-                const int2 r = mm_clipped_rows(a.offsets, ex[i], a.rows);
+                const int2 r = mm_clipped_rows(a.offsets, ex[i], rows);
                 eb[i] = r.x;
                 ne[i] = r.y;
             }

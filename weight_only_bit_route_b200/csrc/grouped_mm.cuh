@@ -87,14 +87,15 @@ int launch_grouped_wgrad(const WgradProblem& p, cudaStream_t s);
 
 // Rows to 8 bits: codes [rows, cols], scales [rows].  With row_slot and top_k, row r reads row row_slot[r] / top_k of
 // the nsrc rows of x; with row_slot and row_w (one or the other), the scale is multiplied by row_w[row_slot[r]], slots
-// below rows.  With nrows (device), rows from *nrows on are left alone.  status nullable.
+// below rows.  With offsets (device), rows outside [offsets[0], offsets[E]) are left alone.  status nullable.
 int launch_quant_int8(const void* x, bool f16, int64_t rows, int64_t cols, const int32_t* row_slot, int top_k,
-                      int64_t nsrc, const float* row_w, const int32_t* nrows, int8_t* codes, float* scales,
+                      int64_t nsrc, const float* row_w, const int32_t* offsets, int E, int8_t* codes, float* scales,
                       int32_t* status, cudaStream_t s);
 // Rows of codes and their scales by slot, as above, from the nsrc rows src, src_scales.  A row of scale NaN is recorded
 // as MOE_ERR_NONFINITE.
 int launch_gather_int8(const int8_t* src, const float* src_scales, int rows, int cols, const int32_t* row_slot, int top_k,
-                       int nsrc, const int32_t* nrows, int8_t* codes, float* scales, int32_t* status, cudaStream_t s);
+                       int nsrc, const int32_t* offsets, int E, int8_t* codes, float* scales, int32_t* status,
+                       cudaStream_t s);
 
 // One-time set-up of a kernel on the current device: its shared-memory attribute; *sms: the device's SM count.
 int mm_kernel_ready(const void* kernel, int smem_bytes, int* sms);

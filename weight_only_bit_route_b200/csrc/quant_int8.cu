@@ -47,7 +47,7 @@ template <bool F16, int TPR>           // TPR threads per row: 32 or the block
 __global__ void __launch_bounds__(Q8_THREADS) quant_int8_kernel(const uint16_t* __restrict__ x, long long cols,
                                                                const int32_t* __restrict__ row_slot, int top_k,
                                                                long long nsrc, const float* __restrict__ row_w,
-                                                               const int32_t* __restrict__ nrows,
+                                                               const int32_t* __restrict__ offsets, int E,
                                                                int8_t* __restrict__ codes, float* __restrict__ scales,
                                                                int32_t* status, long long rows) {
     constexpr int kKeep = TPR == 32 ? 8 : 4;                          // 16-byte chunks per thread kept in registers
@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(Q8_THREADS) quant_int8_kernel(const uint16_t* 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the product's weights need nothing from here
     const long long row = (long long)blockIdx.x * (Q8_THREADS / TPR) + threadIdx.x / TPR;
-    if (row >= rows || (nrows && row >= *nrows)) return;                               // behind the last expert's rows
+    if (row >= rows || (offsets && (row < offsets[0] || row >= offsets[E]))) return;  // a row of no expert
     const long long n = cols / 8;
     uint2* dst = reinterpret_cast<uint2*>(codes + row * cols);
     long long src = row;
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(Q8_THREADS) quant_int8_kernel(const uint16_t* 
 }
 
 int launch_quant_int8(const void* x, bool f16, int64_t rows, int64_t cols, const int32_t* row_slot, int top_k,
-                      int64_t nsrc, const float* row_w, const int32_t* nrows, int8_t* codes, float* scales,
+                      int64_t nsrc, const float* row_w, const int32_t* offsets, int E, int8_t* codes, float* scales,
                       int32_t* status, cudaStream_t s) {
     if (rows <= 0) return MOE_OK;
     const bool warp = rows >= Q8_WARP_ROWS && cols <= Q8_WARP_COLS;
@@ -140,20 +140,20 @@ int launch_quant_int8(const void* x, bool f16, int64_t rows, int64_t cols, const
                   : (f16 ? quant_int8_kernel<true, Q8_THREADS> : quant_int8_kernel<false, Q8_THREADS>);
     const int64_t blocks = warp ? (rows + Q8_THREADS / 32 - 1) / (Q8_THREADS / 32) : rows;
     return mm_launch_cfg(k, dim3(unsigned(blocks)), dim3(Q8_THREADS), 0, 1, s, static_cast<const uint16_t*>(x),
-                         (long long)cols, row_slot, top_k, (long long)nsrc, row_w, nrows, codes, scales, status, (long long)rows);
+                         (long long)cols, row_slot, top_k, (long long)nsrc, row_w, offsets, E, codes, scales, status, (long long)rows);
 }
 
 // One block per row, 16 bytes per thread and step.
 __global__ void __launch_bounds__(Q8_THREADS) gather_int8_kernel(const int8_t* __restrict__ src,
                                                                  const float* __restrict__ src_scales, int cols,
                                                                  const int32_t* __restrict__ row_slot, int top_k, int nsrc,
-                                                                 const int32_t* __restrict__ nrows,
+                                                                 const int32_t* __restrict__ offsets, int E,
                                                                  int8_t* __restrict__ codes, float* __restrict__ scales,
                                                                  int32_t* status) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int row = blockIdx.x;
-    if (row >= *nrows) return;
+    if (row < offsets[0] || row >= offsets[E]) return;
     const long long t = q8_source(row_slot[row], top_k, nsrc);
     if (threadIdx.x == 0) {
         const float scale = t < 0 ? 0.f : src_scales[t];
@@ -167,9 +167,10 @@ __global__ void __launch_bounds__(Q8_THREADS) gather_int8_kernel(const int8_t* _
 }
 
 int launch_gather_int8(const int8_t* src, const float* src_scales, int rows, int cols, const int32_t* row_slot, int top_k,
-                       int nsrc, const int32_t* nrows, int8_t* codes, float* scales, int32_t* status, cudaStream_t s) {
+                       int nsrc, const int32_t* offsets, int E, int8_t* codes, float* scales, int32_t* status,
+                       cudaStream_t s) {
     return mm_launch_cfg(gather_int8_kernel, dim3(unsigned(rows)), dim3(Q8_THREADS), 0, 1, s, src, src_scales, cols,
-                         row_slot, top_k, nsrc, nrows, codes, scales, status);
+                         row_slot, top_k, nsrc, offsets, E, codes, scales, status);
 }
 
 // Per device and kernel: the shared-memory attribute, set once under a lock.
