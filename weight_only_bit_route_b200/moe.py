@@ -118,6 +118,8 @@ def _stream():
 
 def _on(dev, fn, call, *args):
     """The call with the tensors' device current, on its current stream."""
+    if dev < 0:
+        raise MoEError(f"{fn}: tensors on a CUDA device", -1)
     if _current_device() == dev:
         code = call(*args, _raw_stream(dev))
     else:
