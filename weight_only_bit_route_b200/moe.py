@@ -268,6 +268,8 @@ def grouped_down(h_perm, offsets, row_slot, topk_w, down, ws, out=None):
     return y
 
 
+# The 16-bit products.  Like every call of this module they record no history for autograd: for a training step they go
+# into a torch.autograd.Function, grouped_mm as its forward, grouped_mm_dgrad and grouped_mm_wgrad as its backward.
 _BF16, _F16, _F32, _I32, _U8 = torch.bfloat16, torch.float16, torch.float32, torch.int32, torch.uint8
 
 
@@ -292,7 +294,7 @@ def _mm_out(fn, out, shape, dtype, like):
 
 def grouped_mm(x, w, offsets, ws, out=None):
     """y[r] = w[e] x[r] for the rows r of each expert e (bf16 or fp16): x [rows, in], w [E, out, in] -> [rows, out].
-    Rows outside every expert are not written."""
+    Rows outside every expert are not written.  No autograd history is recorded."""
     sx, sw, so = x.shape, w.shape, offsets.shape
     ok = len(sx) == 2 and len(sw) == 3 and len(so) == 1 and sw[0] == so[0] - 1 and sw[2] == sx[1] and sx[0] < 1 << 31
     dev = _mm_check("moe_grouped_mm", x, w, offsets, ws, ok, "x [rows, in], w [E, out, in]")
