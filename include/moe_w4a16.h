@@ -326,7 +326,7 @@ int moe_grouped_w4a16_down(const void* h_perm, const int32_t* expert_offsets,
  * of the tensors.  Offsets that decrease or leave [0, rows] are recorded as
  * MOE_ERR_DEVICE_INDEX; each then counts as the largest up to it, clipped to
  * [0, rows], so that no two experts share a row.  Results do not depend on the order in
- * which tiles run; accumulate takes magnitudes below 2^-126 for zero.  Outputs
+ * which tiles run; accumulate may take magnitudes below 2^-126 for zero.  Outputs
  * must not overlap inputs.  ws: at least 1024 bytes (the control block), zero-filled
  * once; it holds no intermediate results. */
 int moe_grouped_mm(const void* x, const int32_t* expert_offsets, int rows, const void* w, int E,

@@ -708,17 +708,19 @@ static int64_t mm_row_blocks(const MmProblem& p, int nt) {
 // -> 1536, us, single / pair): 352 experts of 47 rows 682 / 725 in bf16 (Zipf load 772 / 760), int8 gate/up 721 / 711
 // (775 / 728), int8 down 368 / 375 (442 / 403); 44 experts of 1490 rows 1122 / 629; one expert of 300 rows
 // 14 / 20, of 1000 rows (24 pair tiles) 30 / 27, of 3000 57 / 29; four of 150 rows (24 pair tiles, K 2048) 11 / 14.
-// (Tiles of 16 rows were never faster than those of 64: 8 tokens over 352 experts 121 us against 117.)
+// (Tiles of 16 rows were never faster than those of 64: 8 tokens over 352 experts 121 us against 117.)  The counts here and
+// in mm_split are those of the whole part, 148 SMs; with fewer the launches adapt, the choice stays, at a cost in time alone.
 static bool mm_pair(const MmProblem& p) {
     return p.rows > (p.i8 ? 32 : 64) * int64_t(p.E) && mm_row_blocks(p, 256) * ((mm_mdim(p) + 255) / 256) >= 37;
 }
-// K slices per stage: two where the stage then still fits the ring four times
+// 128-byte slices of K per stage: two; gate/up, with two weight matrices in a stage, one.  Stages in the ring: 4 (gate/up
+// 5) on single CTAs, 3 in split tiles, 3 (gate/up 4) on pairs.
 static int mm_slices(const MmProblem& p) { return p.w1 ? 1 : 2; }
 // Few tiles leave SMs idle: then clusters of 2, 4 or 8 CTAs (gate/up: 4 at most) share each tile's K, as many as
 // 148, 132 or 120 SMs hold at once, while each CTA still has two stages of K (one expert, 4096 -> 1536: 8 rows 18 us
 // without, 8 with; int8 gate/up of 61 rows 18 / 12).  Pairs of CTAs also turn two rounds of long tiles, the second at
-// most half full, into one and a half (two tokens over 16 experts of 4096 -> 1536, bf16: 43 us / 37; one expert of
-// 1000 rows 30 / 26; but clusters of 4 over several rounds lose: one token, int8 gate/up, 19 / 32, and so do short
+// most half full, into one and a half (two tokens that reach 16 of 352 experts of 4096 -> 1536, bf16: 43 us / 37; one
+// expert of 1000 rows 30 / 26; but clusters of 4 over several rounds lose: one token, int8 gate/up, 19 / 32, and so do short
 // tiles, 16 experts of 1536 -> 4096 in int8 19 / 26, and gate/up, 28 / 33).
 static int mm_split(const MmProblem& p, int* tiles) {
     const int kdim = p.grad ? p.out_dim : p.in_dim;

@@ -3,14 +3,14 @@
 // (0 for an expert without rows; with `accumulate` the sum is added to dw).
 //
 // The contraction runs along the rows, and both operands are stored row by row, so both enter the MMA stored
-// along M (dy: 128 output features per CTA) and N (x: NT input features): 128-byte rows of 64 features, one per
+// along M (dy: 128 output features per CTA) and N (x: 256 input features): 128-byte rows of 64 features, one per
 // row r, as TMA lays them down.  Nothing is transposed in memory.
 //
 // A K block is 64 rows.  The expert's last block also brings rows of the next expert: the MMAs stop at the 16-row
 // step that holds the last row, and the rows between it and the step's end are overwritten with zeros in shared
 // memory, in both operands (a zero in one alone would still meet an infinity or a NaN in the other).
 //
-// A tile is (expert, 128 * CG output features, NT input features); a persistent CTA (or pair) takes a fixed
+// A tile is (expert, 128 * CG output features, 256 input features); a persistent CTA (or pair) takes a fixed
 // sequence of them.  Warp roles: 0 and 3 TMA producers of dy and x, 1 MMA issuer (in a pair: the first CTA's), 2 zeroes the last block's
 // rows, 4-11 epilogue: tensor memory -> registers -> shared memory -> tile store (or fp32 reduction), which
 // clips at the tensor's edges.  The tensor core's fp32 sums are cut off rather than rounded, an error that grows with
@@ -30,11 +30,12 @@ namespace moe {
 
 constexpr int WG_THREADS = 384;
 constexpr int WG_EPI_WARPS = 8;
-// NT: input features per tile; CG: CTAs per tile; Z: CTAs that share a tile's rows
+constexpr int WG_NT = 256;                  // input features per tile
+// CG: CTAs per tile; Z: CTAs that share a tile's rows
 
-template <int NT, int CG, int Z>
+template <int CG, int Z>
 struct WgCfg {
-    static constexpr int kBoxesB = NT / CG / 64;                  // 64-feature boxes of x this CTA stages
+    static constexpr int kBoxesB = WG_NT / CG / 64;               // 64-feature boxes of x this CTA stages
     static constexpr int kBox = 64 * 128;
     static constexpr int kStage = (2 + kBoxesB) * kBox;
     // per epilogue warp: 32-row x 128-byte buffers; a pair's tiles are long, and the room serves the operands better
@@ -42,9 +43,9 @@ struct WgCfg {
     static constexpr int kOutBytes = WG_EPI_WARPS * kOutBufs * 4096;
     static constexpr int kMaxStages = 6, kMinStages = (208 * 1024 - kOutBytes) / kStage;      // (with the largest table)
     static constexpr int kFixed = kOutBytes + 1024;               // beside the stages and 16 bytes per expert
-    static constexpr int kHalf = NT / 2;                          // columns of one epilogue warp
+    static constexpr int kHalf = WG_NT / 2;                       // columns of one epilogue warp
     static constexpr int kChunk = 8;                              // K blocks summed in tensor memory at a time
-    static constexpr int kTmem = 2 * NT;
+    static constexpr int kTmem = 2 * WG_NT;
     static_assert(Z == 1 || (CG == 1 && (Z - 1) * (kHalf / Z) * 4 * 32 * WG_EPI_WARPS <= kMinStages * kStage),
                   "split rows: the partial sums fit the ring");
     static_assert(kBoxesB % 2 == 0, "one copy brings two boxes");
@@ -73,14 +74,14 @@ __device__ __forceinline__ uint32_t wg_pair(float lo, float hi, int f16) {
 __device__ __forceinline__ void wg_cluster_step() {
     asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
 }
-template <int W, int Z, int N>
+template <int W, int N>
 __device__ __forceinline__ float4 wg_pick(const float (&sum)[N], int r, int j) {      // r and j are constants after unrolling
     return make_float4(sum[r * W + 4 * j], sum[r * W + 4 * j + 1], sum[r * W + 4 * j + 2], sum[r * W + 4 * j + 3]);
 }
 
-template <int NT, int CG, int Z>
+template <int CG, int Z>
 __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_constant__ WgArgs a) {
-    using C = WgCfg<NT, CG, Z>;
+    using C = WgCfg<CG, Z>;
     constexpr int SM = C::kMaxStages;
     const uint32_t S = uint32_t(a.stages);
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -92,7 +93,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = CG == 2 ? g_cta_rank() : 0u;
     const uint32_t zr = Z > 1 ? g_cta_rank() : 0u;          // this CTA's share of a tile's rows
-    const int MT = (a.out_dim + 128 * CG - 1) / (128 * CG), NTN = (a.in_dim + NT - 1) / NT;
+    const int MT = (a.out_dim + 128 * CG - 1) / (128 * CG), NTN = (a.in_dim + WG_NT - 1) / WG_NT;
 
     if (warp == 4 && (lane == 2 || (lane < 2 && a.rows > 0))) g_prefetch_map(lane == 0 ? &a.a : lane == 1 ? &a.b : &a.d);
     if (tid == 0) {
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
             t.n = min(per, t.n - first);
         }
         t.m0 = (local % MT) * (128 * CG);
-        t.n0 = (local / MT) * NT;
+        t.n0 = (local / MT) * WG_NT;
         return t;
     };
     auto fail = [&]() {
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
         for (int i = 0; i < seq.count && ok && !g_aborted(&s_ab); i++) {
             const Tile T = tile_of(seq.tile(i));
             const int KB = (T.n + 63) / 64;
-            const int x0 = isb ? T.n0 + int(rank) * (NT / CG) : T.m0 + int(rank) * 128;
+            const int x0 = isb ? T.n0 + int(rank) * (WG_NT / CG) : T.m0 + int(rank) * 128;
             for (int kb = 0; kb < KB; kb++, it++) {
                 if (!g_wait_long(g_smem(&empty[s]), ph ^ 1, &s_ab)) {      // (a new barrier's phase before the first is over)
                     ok = false;
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
     } else if (warp == 1 && rank == 0) {
         // ---------------- MMA issuer (whole warp, one lane issues) ----------------
         if (s_hold && !g_wait_long(g_smem(&hold_bar), 0, &s_ab)) fail();
-        const uint32_t idesc = g_idesc(NT, a.f16 != 0, 128 * CG) | G_IDESC_A_MN | G_IDESC_B_MN;
+        const uint32_t idesc = g_idesc(WG_NT, a.f16 != 0, 128 * CG) | G_IDESC_A_MN | G_IDESC_B_MN;
         uint32_t s = 0, ph = 0;
         int t = 0;
         bool ok = true;
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
             const int KB = (T.n + 63) / 64;
             for (int kb = 0; kb < KB && ok; kb++) {
                 const int kc = kb % C::kChunk;
-                const uint32_t d = tmem + (t & 1) * NT;
+                const uint32_t d = tmem + (t & 1) * WG_NT;
                 if (kc == 0) {
                     if (t >= 2 && !g_wait_long(g_smem(&acc_empty[t & 1]), ((t >> 1) - 1) & 1, &s_ab)) {
                         ok = false;
@@ -341,7 +342,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
                     break;
                 }
                 g_fence_after();
-                const uint32_t acc = tmem + lane_addr + (t & 1) * NT + c0;
+                const uint32_t acc = tmem + lane_addr + (t & 1) * WG_NT + c0;
 #pragma unroll
                 for (int c = 0; c < C::kHalf; c += 16) {
                     uint32_t v[16];
@@ -382,7 +383,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
 #pragma unroll
                     for (int j = 0; j < W / 4; j++) {
                         float4 v;
-                        if (r == int(zr)) v = wg_pick<W, Z>(sum, r, j);
+                        if (r == int(zr)) v = wg_pick<W>(sum, r, j);
                         else v = *reinterpret_cast<const float4*>(p + j * 512);
                         mine[4 * j] += v.x;
                         mine[4 * j + 1] += v.y;
@@ -511,10 +512,10 @@ __global__ void __launch_bounds__(WG_THREADS, 1) wgrad_kernel(const __grid_const
     }
 }
 
-template <int NT, int CG, int Z>
+template <int CG, int Z>
 static int wg_launch(const WgArgs& a, cudaStream_t s) {
-    using C = WgCfg<NT, CG, Z>;
-    auto k = wgrad_kernel<NT, CG, Z>;
+    using C = WgCfg<CG, Z>;
+    auto k = wgrad_kernel<CG, Z>;
     // Dynamic shared memory: what a block may have beside the kernel's static 1 KB.
     constexpr int kRoom = 227 * 1024 - 1024;
     static_assert(C::kMinStages * C::kStage + C::kFixed + 16 * kMaxE <= kRoom, "the largest table fits");
@@ -524,7 +525,7 @@ static int wg_launch(const WgArgs& a, cudaStream_t s) {
     WgArgs args = a;
     args.stages = std::min(C::kMaxStages, (kRoom - C::kFixed - 16 * a.E) / C::kStage);
     const int smem = args.stages * C::kStage + C::kFixed + 16 * a.E;
-    const int tiles = a.E * ((a.out_dim + 128 * CG - 1) / (128 * CG)) * ((a.in_dim + NT - 1) / NT);
+    const int tiles = a.E * ((a.out_dim + 128 * CG - 1) / (128 * CG)) * ((a.in_dim + WG_NT - 1) / WG_NT);
     return mm_launch_cfg(k, dim3(Z > 1 ? tiles * Z : sms / CG * CG), dim3(WG_THREADS), smem, CG * Z, s, args);
 }
 
@@ -561,15 +562,16 @@ int launch_grouped_wgrad(const WgradProblem& p, cudaStream_t s) {
     a.f16 = p.f16;
     a.out_f32 = p.out_f32;
     a.accumulate = p.accumulate;
+    // (The counts below are those of the whole part, 148 SMs.)
     // Few tiles (33 clusters of four run at once) and many rows: clusters of four share a tile's rows (one expert of
     // 8192 rows, 1000 x 264: 29 us).
     const int64_t tiles = int64_t(p.E) * ((a.out_dim + 127) / 128) * ((a.in_dim + 255) / 256);
-    if (tiles * 4 <= 132 && p.rows >= 512 * int64_t(p.E)) return wg_launch<256, 1, 4>(a, s);
+    if (tiles * 4 <= 132 && p.rows >= 512 * int64_t(p.E)) return wg_launch<1, 4>(a, s);
     // Up to 128 rows per expert the tiles are short and the writes bound them: single CTAs keep more of them in flight;
     // above, a pair loads a quarter less per tile.  Measured (4096 x 1536, bf16, us, single / pair): 352 experts of 47
     // rows 836 / 1044; 44 of 93 rows 138 / 162, of 186 182 / 166, of 372 281 / 236, of 1490 852 / 686.
     const int64_t pairs = int64_t(p.E) * ((a.out_dim + 255) / 256) * ((a.in_dim + 255) / 256);
-    return p.rows > 128 * int64_t(p.E) && pairs >= 37 ? wg_launch<256, 2, 1>(a, s) : wg_launch<256, 1, 1>(a, s);
+    return p.rows > 128 * int64_t(p.E) && pairs >= 37 ? wg_launch<2, 1>(a, s) : wg_launch<1, 1>(a, s);
 }
 
 }  // namespace moe
