@@ -30,8 +30,8 @@
 // K = 4096 723 / 727 / 740 us, K = 1536 722 / 736 / 757 (chunks of 1536: 730); 8 tokens over 352 experts 118.7 / 119.4 / 119.8.
 //
 // Bound by the weight stream up to some hundred rows per expert (352 experts of 4096 x 1536: 8 tokens 117 us in bf16,
-// 114 us for int8 gate and up, 6.3 and 6.5 TB/s; 2048 tokens 682 us, 6.8 TB/s), by the tensor pipe and the power cap
-// above (65,536 rows over 44 experts: 1360 TFLOP/s in a burst, 1150 sustained at 1.1 to 1.2 GHz, the pipe 83 % active).
+// 114 us for int8 gate and up, 6.3 and 6.5 TB/s; 2048 tokens 694 us, 6.6 TB/s), by the tensor pipe and the power cap
+// above (65,536 rows over 44 experts: 1340 TFLOP/s in a burst, 1130 sustained at 1.1 to 1.2 GHz, the pipe 80 % active).
 //
 // Every wait is bounded (moe_set_wait_limit).  On expiry the kernel records MOE_ERR_TIMEOUT, stops issuing work,
 // waits (bounded) for its copies and MMAs in flight, frees its tensor memory and returns.
@@ -705,9 +705,9 @@ static int64_t mm_row_blocks(const MmProblem& p, int nt) {
 
 // Tiles of 256 rows x 256 features on CTA pairs when the experts hold more than 64 rows on average (int8: 32, whose
 // MMAs take half the time) and half the pairs get a tile; else 64 rows x 128 features on single CTAs.  Measured (4096
-// -> 1536, us, single / pair): 352 experts of 47 rows 682 / 725 in bf16 (Zipf load 772 / 760), int8 gate/up 721 / 711
-// (775 / 728), int8 down 368 / 375 (442 / 403); 44 experts of 1490 rows 1122 / 629; one expert of 300 rows
-// 14 / 20, of 1000 rows (24 pair tiles) 30 / 27, of 3000 57 / 29; four of 150 rows (24 pair tiles, K 2048) 11 / 14.
+// -> 1536, us, single / pair): 352 experts of 47 rows 696 / 763 in bf16 (Zipf load 782 / 780), int8 gate/up 721 / 711
+// (775 / 728), int8 down 368 / 375 (442 / 403); 44 experts of 1490 rows 1150 / 583; one expert of 300 rows
+// 16 / 25, of 1000 rows (24 pair tiles) 29 / 29, of 3000 61 / 31; four of 150 rows (24 pair tiles, K 2048) 12 / 15.
 // (Tiles of 16 rows were never faster than those of 64: 8 tokens over 352 experts 121 us against 117.)  The counts here and
 // in mm_split are those of the whole part, 148 SMs; with fewer the launches adapt, the choice stays, at a cost in time alone.
 static bool mm_pair(const MmProblem& p) {

@@ -17,9 +17,10 @@
 // the number of rows; so only 512 rows are summed in tensor memory at a time, and the epilogue adds those partial
 // sums in fp32 registers, rounded to nearest (a 65,536-row batch over 44 experts: 4.4e-6 of the result in one sum).
 //
-// Bound by the writes when experts hold few rows (352 experts of 47 rows, 4096 x 1536, bf16: 846 us, 5.2 TB/s written),
-// by the operands' latency and the power cap when they hold many (65,536 rows over 44 experts, fp32: 751 us in a
-// burst, 1100 TFLOP/s, the tensor pipe 68 % active).
+// Bound by the writes when experts hold few rows: 352 experts of 47 rows, 4096 x 1536, bf16, take 840 us in a burst and
+// 977 in a loop, where the power cap counts; the stores alone (the same call without rows) 820 and 833, 5.4 TB/s.  With
+// many rows by the operands' latency and the power cap: 65,536 rows over 44 experts, fp32, 760 us in a burst, 1085 TFLOP/s,
+// the tensor pipe 68 % active, and 835 in a loop.  (128 sums a thread: ptxas keeps 7 to 13 words of the rest in local memory.)
 #include <algorithm>
 #include <cstring>
 
